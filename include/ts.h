@@ -313,6 +313,98 @@ TS_API ts_status_t ts_append_kv(const ts_kv_t *kv, int64_t *seq_offsets, void *k
                                 const void *k_new, const void *v_new, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * New tokens of many requests: prompts, chunks of prompts, single tokens.
+ * ts_extend_pages finds room for them in a paged cache, ts_write_kv brings
+ * their K and V rows there, ts_dense_attn attends with their queries over
+ * all of each sequence's tokens (the attention that a selection replaces;
+ * TokenSelect README, "Result", compares with it).  A decode step can follow
+ * on the same cache.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Block table, slots and offsets of a paged cache whose sequence b holds
+ * cached[b] tokens and gains fresh[b].  With P = page_size:
+ *   have_b = ceil(cached[b] / P), new_b = ceil((cached[b] + fresh[b]) / P) - have_b,
+ *   first_b = sum_{a < b} new_a
+ *   page_table[b][have_b + i]  = free_pages[first_b + i]            (i < new_b)
+ *   slots[q_offsets[b] + j]    = page_table[b][t / P] * P + t % P,  t = cached[b] + j
+ *   q_offsets[b]   = sum_{a < b} fresh[a]              (device int64 [batch + 1])
+ *   seq_offsets[b] = sum_{a < b} cached[a] + fresh[a]  (device int64 [batch + 1])
+ *   *pages_used    = sum_b new_b                       (device int64)
+ * so the caller's free list goes on at pages_used.  Entries of the table
+ * outside the new pages are left as they were; slots behind the last new
+ * token are -1.  The lengths are read on the device (a captured graph serves
+ * other lengths) and nothing is kept: a second call with the same inputs
+ * writes the same.
+ *   cached, fresh   device int64 [batch], in [0, 2^31) (outside: the nearest)
+ *   page_size       a power of two in [8, 4096]
+ *   free_pages      device int32 [n_free], pages of the pool, distinct
+ *   page_table      device int32 [batch][page_table_stride], in and out
+ *   slots           device int64 [n_slots]: n_slots at least the new tokens
+ * When the free list is too short (pages_used > n_free), or holds a page
+ * outside [0, pool_pages), the entries concerned and their tokens' slots are
+ * -1; tokens past page_table_stride pages get the slot -1; tokens and pages
+ * that begin at or behind n_slots (q_offsets[batch] > n_slots) are left out.
+ * At most 1024 sequences.  The arrays must not overlap.
+ */
+TS_API ts_status_t ts_extend_pages(int32_t batch, const int64_t *cached, const int64_t *fresh, int32_t page_size,
+                                   const int32_t *free_pages, int64_t n_free, int64_t pool_pages,
+                                   int32_t *page_table, int32_t page_table_stride, int64_t *seq_offsets,
+                                   int64_t *q_offsets, int64_t *slots, int64_t n_slots, int64_t *pages_used,
+                                   void *stream);
+
+/*
+ * K and V rows of n_new tokens to their slots: token row slots[r] of the
+ * cache (of the pool, if paged) receives row r of k_new and v_new.  Rows whose
+ * slot is outside the cache's token rows (negative, as behind the last token
+ * of ts_extend_pages' slots; or too large) go nowhere.  Of two rows with the
+ * same slot each 16-byte piece is one's or the other's.
+ *   k_cache, v_cache  kv->k and kv->v, writable
+ *   k_new, v_new      device bf16 [n_new][h_kv][head_dim], 16-byte aligned,
+ *                     new_stride_tok elements (a multiple of 8, at least
+ *                     h_kv * head_dim) from token to token
+ *   slots             device int64 [n_new]
+ * The new rows must not overlap the cache.
+ */
+TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, const void *k_new,
+                               const void *v_new, int64_t new_stride_tok, const int64_t *slots, int64_t n_new,
+                               void *stream);
+
+/*
+ * Causal attention of each sequence's newest tokens over all of its tokens.
+ * Sequence b has f_b = q_offsets[b+1] - q_offsets[b] query rows, those of its
+ * last f_b tokens (their K and V are in the cache already); row i of them
+ * sits at p = n_b - f_b + i and sees the tokens 0..p:
+ *   out[r,h,:] = sum_{j <= p} softmax_j(scale * q[r,h,:] . K[b,j,h/G,:]) * V[b,j,h/G,:]
+ *   lse[r,h]   = log sum_{j <= p} exp(scale * q[r,h,:] . K[b,j,h/G,:])
+ * with r = q_offsets[b] + i.  f_b = n_b is a whole prompt, f_b = 1 a decode
+ * step, f_b = 0 a sequence without queries; they may stand side by side.  A
+ * row that sees nothing (p < 0) gives zeros and -inf.  The scores, the
+ * running maximum and sum and the weighted sums are fp32; the weights are
+ * rounded to bf16 for the product with V, and out at the end.  Tokens that a
+ * row does not see have no effect on it, whatever their K and V hold.
+ *   q              device bf16 [q_offsets[batch]][h_q][head_dim], 16-byte
+ *                  aligned, q_stride_tok elements (a multiple of 8, at least
+ *                  h_q * head_dim) from token to token
+ *   q_offsets      device int64 [batch+1], non-decreasing, [0] == 0
+ *   q_offsets_host host copy of the same (sizing and checks)
+ *   out            device bf16 [q_offsets[batch]][h_q][head_dim], contiguous,
+ *                  16-byte aligned; rows behind the last are left as they were
+ *   lse            device float32 [q_offsets[batch]][h_q] or NULL
+ *   ws             workspace of ts_dense_attn_workspace_bytes, initialised
+ *                  once (ts_workspace_init); ts_get_device_status reads it
+ * The cache may be packed, growing (capacity; the length is read on the
+ * device) or paged (a table entry outside the pool: no access outside the
+ * pool, results not defined).  At most 2^24 query rows.
+ */
+TS_API size_t ts_dense_attn_workspace_bytes(const ts_kv_t *kv, const int64_t *q_offsets_host);
+TS_API ts_status_t ts_dense_attn(const ts_kv_t *kv, const void *q, int64_t q_stride_tok, const int64_t *q_offsets,
+                                 const int64_t *q_offsets_host, void *out, float *lse, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/*
  * Number of kernels one ts_decode_step call on this cache launches (for
  * launch accounting and profiling), or -1 with ts_last_error set when the
  * cache description or the selection sizes are invalid.  Host only; touches

@@ -90,6 +90,11 @@ _SIGS = {
     "ts_quest_metadata_update": (ctypes.c_int, [_KV, _I32, ctypes.c_int64, _P, _P, _P]),
     "ts_quest_score": (ctypes.c_int, [_KV, _P, _I32, _P, _P, _P, _P]),
     "ts_quest_select": (ctypes.c_int, [_KV, _P, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "ts_extend_pages": (ctypes.c_int, [_I32, _P, _P, _I32, _P, ctypes.c_int64, ctypes.c_int64, _P, _I32, _P, _P, _P,
+                                       ctypes.c_int64, _P, _P]),
+    "ts_write_kv": (ctypes.c_int, [_KV, _P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P]),
+    "ts_dense_attn_workspace_bytes": (_SZ, [_KV, _P]),
+    "ts_dense_attn": (ctypes.c_int, [_KV, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _SZ, _P]),
     "ts_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ts_last_error": (ctypes.c_char_p, []),
 }
@@ -344,6 +349,126 @@ def ts_quest_select(kv: KVCache, scores, page_size: int, k: int, n_sink: int, n_
                                 _ptr(ids), _ptr(count), _stream(stream)))
 
 
+# ---- new tokens of many requests: room, cache rows, attention ----
+
+def _on_device(name, t, dtype, device, shape=None):
+    """A contiguous tensor of this type on the current CUDA device (and of
+    this shape): what the kernels below take by address alone."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("libts computes on the GPU only; %s is a %s tensor" % (name, t.device))
+    if t.device != device:
+        raise ValueError("%s is on %s, the call runs on %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have the shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _token_rows(name, t, heads: int, d: int, device) -> int:
+    """[tokens, heads, d] bf16 with contiguous heads; returns the token stride
+    (a view of a wider projection's output has more than heads * d)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("libts computes on the GPU only; %s is a %s tensor" % (name, t.device))
+    if t.device != device:
+        raise ValueError("%s is on %s, the call runs on %s" % (name, t.device, device))
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be bf16" % name)
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError("%s must be [tokens, %d, %d] (got %s)" % (name, heads, d, tuple(t.shape)))
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError("%s must have contiguous heads of contiguous channels" % name)
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _current_device():
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def _cache_on(kv: KVCache, device):
+    if kv.k.device != device:
+        raise ValueError("the cache is on %s, the call runs on %s" % (kv.k.device, device))
+
+
+def ts_extend_pages(cached, fresh, page_size: int, free_pages, pool_pages: int, page_table, seq_offsets, q_offsets,
+                    slots, pages_used, stream=None):
+    """Block table, slots and offsets of a paged cache from the requests'
+    lengths: cached, fresh int64 [B]; free_pages int32; page_table int32
+    [B, stride], its new entries written; seq_offsets, q_offsets int64 [B+1],
+    slots int64 [at least the new tokens] and pages_used int64 [1] written."""
+    if not isinstance(cached, torch.Tensor) or not cached.is_cuda:
+        raise ValueError("libts computes on the GPU only; cached must be a CUDA tensor")
+    dev, B = _current_device(), cached.shape[0] if cached.dim() == 1 else -1
+    for name, t in (("cached", cached), ("fresh", fresh)):
+        _on_device(name, t, torch.int64, dev, (B,))
+    for name, t in (("seq_offsets", seq_offsets), ("q_offsets", q_offsets)):
+        _on_device(name, t, torch.int64, dev, (B + 1,))
+    _on_device("free_pages", free_pages, torch.int32, dev, (free_pages.numel(),))
+    _on_device("slots", slots, torch.int64, dev, (slots.numel(),))
+    _on_device("pages_used", pages_used, torch.int64, dev, (1,))
+    _on_device("page_table", page_table, torch.int32, dev)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [batch, stride]")
+    _check(_lib.ts_extend_pages(B, _ptr(cached), _ptr(fresh), int(page_size), _ptr(free_pages), free_pages.numel(),
+                                int(pool_pages), _ptr(page_table), page_table.shape[1], _ptr(seq_offsets),
+                                _ptr(q_offsets), _ptr(slots), slots.numel(), _ptr(pages_used), _stream(stream)))
+
+
+def ts_write_kv(kv: KVCache, k_new, v_new, slots, stream=None):
+    """K and V rows of new tokens ([n, h_kv, d] bf16; views of a projection's
+    output, of equal token stride) to the token rows slots (int64 [n]) of the
+    cache; rows with a slot outside the cache go nowhere."""
+    dev = _current_device()
+    _cache_on(kv, dev)
+    st = _token_rows("k_new", k_new, kv.h_kv, kv.head_dim, dev)
+    if v_new.shape != k_new.shape or _token_rows("v_new", v_new, kv.h_kv, kv.head_dim, dev) != st:
+        raise ValueError("k_new and v_new must have the same shape and token stride")
+    _on_device("slots", slots, torch.int64, dev, (k_new.shape[0],))
+    _check(_lib.ts_write_kv(kv.ref(), _ptr(kv.k), _ptr(kv.v), _ptr(k_new), _ptr(v_new), st, _ptr(slots),
+                            k_new.shape[0], _stream(stream)))
+
+
+def ts_dense_attn_workspace_bytes(kv: KVCache, q_offsets_host) -> int:
+    off = _host_offsets(q_offsets_host, kv.batch)
+    n = _lib.ts_dense_attn_workspace_bytes(kv.ref(), off.ctypes.data)
+    if n == 0:
+        raise TsError(TS_ERR_INVALID_ARG, ts_last_error())
+    return int(n)
+
+
+def ts_dense_attn(kv: KVCache, q, q_offsets_dev, q_offsets_host, out, lse, ws, stream=None):
+    """Causal attention of each sequence's newest tokens (q [n, h_q, d] bf16,
+    rows q_offsets[b] .. q_offsets[b+1] of sequence b) over all of its cached
+    tokens; out bf16 [n, h_q, d], lse float32 [n, h_q] or None."""
+    dev = _current_device()
+    _cache_on(kv, dev)
+    off = _host_offsets(q_offsets_host, kv.batch)
+    rows = int(off[-1])
+    st = _token_rows("q", q, kv.h_q, kv.head_dim, dev)
+    _on_device("q_offsets_dev", q_offsets_dev, torch.int64, dev, (kv.batch + 1,))
+    _on_device("out", out, torch.bfloat16, dev)
+    if q.shape[0] < rows or out.dim() != 3 or out.shape[0] < rows or out.shape[1:] != q.shape[1:]:
+        raise ValueError("q and out must hold the %d query rows" % rows)
+    if lse is not None:
+        _on_device("lse", lse, torch.float32, dev)
+        if lse.dim() != 2 or lse.shape[0] < rows or lse.shape[1] != kv.h_q:
+            raise ValueError("lse must be [rows, h_q]")
+    _check(_lib.ts_dense_attn(kv.ref(), _ptr(q), st, _ptr(q_offsets_dev), off.ctypes.data, _ptr(out), _ptr(lse),
+                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _host_offsets(offsets, batch: int) -> np.ndarray:
+    off = np.ascontiguousarray(np.asarray(offsets, dtype=np.int64))
+    if off.shape != (batch + 1,):
+        raise ValueError("offsets must have %d entries (got %s)" % (batch + 1, off.shape))
+    return off
+
+
 def ts_status_string(status: int) -> str:
     return _status_name(status)
 
@@ -416,4 +541,29 @@ def quest_step(kv: KVCache, q, qbuf: QuestBuffers, buf: StepBuffers, stream=None
     ts_quest_score(kv, q, qbuf.page_size, qbuf.kmin, qbuf.kmax, qbuf.scores, stream)
     ts_quest_select(kv, qbuf.scores, qbuf.page_size, buf.k, buf.n_sink, buf.n_local, buf.ids, buf.count, stream)
     ts_sparse_attn(kv, q, buf.ids, buf.count, buf.out, buf.ws, stream)
+    return buf.out
+
+
+class DenseBuffers:
+    """Query offsets (host and device) and device buffers of ts_dense_attn for
+    one cache and one set of new tokens: workspace, out and lse."""
+
+    def __init__(self, kv: KVCache, q_offsets):
+        dev = kv.k.device
+        self.q_offsets_host = _host_offsets(q_offsets.cpu() if isinstance(q_offsets, torch.Tensor) else q_offsets,
+                                            kv.batch)
+        self.q_offsets_dev = torch.from_numpy(self.q_offsets_host).to(dev)
+        self.rows = int(self.q_offsets_host[-1])
+        self.ws = torch.empty(ts_dense_attn_workspace_bytes(kv, self.q_offsets_host), dtype=torch.uint8, device=dev)
+        ts_workspace_init(self.ws)
+        self.out = torch.zeros((self.rows, kv.h_q, kv.head_dim), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros((self.rows, kv.h_q), dtype=torch.float32, device=dev)
+
+
+def chunk_step(kv: KVCache, q, k_new, v_new, slots, buf: DenseBuffers, stream=None):
+    """New tokens of one layer, in stream order: their K and V rows to the
+    slots of the cache (whose lengths count them already), then their attention
+    over the whole of it; the output and its log-sum-exp land in buf."""
+    ts_write_kv(kv, k_new, v_new, slots, stream)
+    ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws, stream)
     return buf.out

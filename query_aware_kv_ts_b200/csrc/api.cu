@@ -415,7 +415,38 @@ ts_status_t make_plan(const ts_kv_t *kv, int capacity, Plan *p)
     return TS_OK;
 }
 
-static ts_status_t check_ws(const Plan &p, void *ws, size_t ws_bytes)
+ts_status_t make_dense_plan(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp)
+{
+    if (q_off == nullptr) {
+        set_error("q_offsets_host is required");
+        return TS_ERR_INVALID_ARG;
+    }
+    if (q_off[0] != 0) {
+        set_error("q_offsets[0] must be 0");
+        return TS_ERR_INVALID_ARG;
+    }
+    const ts_status_t s = make_plan(kv, -1, &dp->p);
+    if (s != TS_OK)
+        return s;
+    dp->max_rows = 0;
+    for (int b = 0; b < kv->batch; ++b) {
+        const int64_t f = q_off[b + 1] - q_off[b];
+        if (f < 0) {
+            set_error("q_offsets must be non-decreasing (sequence %d)", b);
+            return TS_ERR_INVALID_ARG;
+        }
+        dp->max_rows = f > dp->max_rows ? f : dp->max_rows;
+    }
+    dp->rows = q_off[kv->batch];
+    if (dp->rows > kMaxDenseRows) {
+        set_error("%lld query tokens exceed the supported maximum %lld", (long long)dp->rows, (long long)kMaxDenseRows);
+        return TS_ERR_UNSUPPORTED;
+    }
+    dp->total_bytes = 256;
+    return TS_OK;
+}
+
+static ts_status_t check_ws(size_t needed, void *ws, size_t ws_bytes)
 {
     if (ws == nullptr) {
         set_error("workspace is NULL");
@@ -425,11 +456,16 @@ static ts_status_t check_ws(const Plan &p, void *ws, size_t ws_bytes)
         set_error("workspace must be 256-byte aligned");
         return TS_ERR_WORKSPACE;
     }
-    if (ws_bytes < p.total_bytes) {
-        set_error("workspace too small: %zu bytes given, %zu needed", ws_bytes, p.total_bytes);
+    if (ws_bytes < needed) {
+        set_error("workspace too small: %zu bytes given, %zu needed", ws_bytes, needed);
         return TS_ERR_WORKSPACE;
     }
     return TS_OK;
+}
+
+static ts_status_t check_ws(const Plan &p, void *ws, size_t ws_bytes)
+{
+    return check_ws(p.total_bytes, ws, ws_bytes);
 }
 
 // K as a 3-D tensor (channels, tokens, kv heads) for TMA.  fused: boxes of
@@ -898,6 +934,114 @@ ts_status_t ts_append_kv(const ts_kv_t *kv, int64_t *seq_offsets, void *k_cache,
                                   p.Hkv, p.D, kv->capacity, reinterpret_cast<uint32_t *>(ws),
                                   static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TS_OK : cuda_fail(e, "ts_append_kv");
+}
+
+ts_status_t ts_extend_pages(int32_t batch, const int64_t *cached, const int64_t *fresh, int32_t page_size,
+                            const int32_t *free_pages, int64_t n_free, int64_t pool_pages, int32_t *page_table,
+                            int32_t page_table_stride, int64_t *seq_offsets, int64_t *q_offsets, int64_t *slots,
+                            int64_t n_slots, int64_t *pages_used, void *stream)
+{
+    if (batch < 1 || n_free < 0 || n_slots < 0 || pool_pages < 1 || page_table_stride < 1) {
+        set_error("batch, pool_pages and page_table_stride must be >= 1, n_free and n_slots >= 0");
+        return TS_ERR_INVALID_ARG;
+    }
+    if (batch > kMaxBatch) {
+        set_error("batch %d exceeds the supported maximum %d", batch, kMaxBatch);
+        return TS_ERR_UNSUPPORTED;
+    }
+    if (page_size < 8 || (page_size & (page_size - 1)) != 0 || page_size > 4096) {
+        set_error("page_size %d must be a power of two in [8, 4096]", page_size);
+        return TS_ERR_UNSUPPORTED;
+    }
+    if (pool_pages >= (int64_t(1) << 31) / page_size) {
+        set_error("the pool's %lld pages of %d rows must hold below 2^31 rows", (long long)pool_pages, page_size);
+        return TS_ERR_UNSUPPORTED;
+    }
+    if (cached == nullptr || fresh == nullptr || page_table == nullptr || seq_offsets == nullptr ||
+        q_offsets == nullptr || pages_used == nullptr || (n_free > 0 && free_pages == nullptr) ||
+        (n_slots > 0 && slots == nullptr)) {
+        set_error("cached, fresh, free_pages, page_table, seq_offsets, q_offsets, slots and pages_used are required");
+        return TS_ERR_INVALID_ARG;
+    }
+    const int sms = device_sms();
+    if (sms <= 0) {
+        set_error("no CUDA device");
+        return TS_ERR_CUDA;
+    }
+    const cudaError_t e = launch_extend_pages(cached, fresh, batch, page_size, free_pages, n_free, pool_pages,
+                                              page_table, page_table_stride, seq_offsets, q_offsets, slots, n_slots,
+                                              pages_used, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "ts_extend_pages");
+}
+
+ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, const void *k_new, const void *v_new,
+                        int64_t new_stride_tok, const int64_t *slots, int64_t n_new, void *stream)
+{
+    if (n_new < 0 || n_new >= (int64_t(1) << 31)) {
+        set_error("n_new %lld must be in [0, 2^31)", (long long)n_new);
+        return TS_ERR_INVALID_ARG;
+    }
+    if (n_new > 0 && (k_new == nullptr || v_new == nullptr || slots == nullptr ||
+                      ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15u))) {
+        set_error("k_new and v_new must be 16-byte aligned device rows, with one slot each");
+        return TS_ERR_INVALID_ARG;
+    }
+    if (kv != nullptr && (k_cache != kv->k || v_cache != kv->v)) {
+        set_error("k_cache and v_cache must be the cache's own device arrays");
+        return TS_ERR_INVALID_ARG;
+    }
+    if (kv != nullptr && (new_stride_tok % 8 != 0 || new_stride_tok < (int64_t)kv->h_kv * kv->head_dim)) {
+        set_error("new_stride_tok %lld must be a multiple of 8 and at least h_kv * head_dim",
+                  (long long)new_stride_tok);
+        return TS_ERR_INVALID_ARG;
+    }
+    Plan p;
+    const ts_status_t s = make_plan(kv, -1, &p);
+    if (s != TS_OK)
+        return s;
+    if (n_new == 0)
+        return TS_OK;
+    const cudaError_t e = launch_write_kv(p, kv, k_cache, v_cache, k_new, v_new, new_stride_tok, slots, n_new,
+                                          static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "ts_write_kv");
+}
+
+size_t ts_dense_attn_workspace_bytes(const ts_kv_t *kv, const int64_t *q_offsets_host)
+{
+    DensePlan dp;
+    if (make_dense_plan(kv, q_offsets_host, &dp) != TS_OK)
+        return 0;
+    return dp.total_bytes;
+}
+
+ts_status_t ts_dense_attn(const ts_kv_t *kv, const void *q, int64_t q_stride_tok, const int64_t *q_offsets,
+                          const int64_t *q_offsets_host, void *out, float *lse, void *ws, size_t ws_bytes,
+                          void *stream)
+{
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u) {
+        set_error("q and out must be 16-byte aligned");
+        return TS_ERR_INVALID_ARG;
+    }
+    if (kv != nullptr && (q_stride_tok % 8 != 0 || q_stride_tok < (int64_t)kv->h_q * kv->head_dim)) {
+        set_error("q_stride_tok %lld must be a multiple of 8 and at least h_q * head_dim", (long long)q_stride_tok);
+        return TS_ERR_INVALID_ARG;
+    }
+    DensePlan dp;
+    ts_status_t s = make_dense_plan(kv, q_offsets_host, &dp);
+    if (s != TS_OK)
+        return s;
+    if (dp.rows == 0)
+        return TS_OK;
+    if (q == nullptr || q_offsets == nullptr || out == nullptr) {
+        set_error("q, q_offsets and out are required");
+        return TS_ERR_INVALID_ARG;
+    }
+    s = check_ws(dp.total_bytes, ws, ws_bytes);
+    if (s != TS_OK)
+        return s;
+    const cudaError_t e = launch_dense(dp, kv, q, q_stride_tok, q_offsets, out, lse, static_cast<uint8_t *>(ws),
+                                       static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TS_OK : cuda_fail(e, "dense attention launch");
 }
 
 ts_status_t ts_selftest_expire_wait(void *ws, size_t ws_bytes, uint32_t spin_limit, void *stream)

@@ -26,6 +26,7 @@ constexpr int kMaxSelectRanges = 2048;        // ranges per sequence: n <= 4M ca
 constexpr int kAttnThreads = 256;
 constexpr int kAttnRows = 64;         // selected rows per attention CTA (one split)
 constexpr int kMaxCapacity = 16384;   // k + sink + local
+constexpr int64_t kMaxDenseRows = int64_t(1) << 24;   // query tokens of one dense attention call
 constexpr int kFusedRows = 128;       // K rows per stage of the fused scoring kernel (HS heads x T tokens)
 constexpr size_t kFusedPassLogitsBytes = size_t(32) << 20;   // logits one fused-scoring pass may keep in L2
 
@@ -213,6 +214,28 @@ ts_status_t launch_attn_noalloc(const Plan &p, const ts_kv_t *kv, const void *q,
                                 const int32_t *count, float *out, cudaStream_t st);
 
 cudaError_t launch_selftest_wait(uint32_t *ctrl, uint32_t spin_limit, cudaStream_t st);
+
+// New tokens of many requests (pages.cu): block table, slots and offsets from
+// the requests' lengths; K and V rows to their slots.
+cudaError_t launch_extend_pages(const int64_t *cached, const int64_t *fresh, int B, int page_size,
+                                const int32_t *free_pages, int64_t n_free, int64_t pool_pages, int32_t *page_table,
+                                int stride, int64_t *seq_offsets, int64_t *q_offsets, int64_t *slots,
+                                int64_t n_slots, int64_t *pages_used, int sms, cudaStream_t st);
+cudaError_t launch_write_kv(const Plan &p, const ts_kv_t *kv, void *k_cache, void *v_cache, const void *k_new,
+                            const void *v_new, int64_t new_stride_tok, const int64_t *slots, int64_t n_new,
+                            cudaStream_t st);
+
+// Attention of the newest tokens over the whole cache (dense.cu).
+struct DensePlan {
+    Plan p;
+    int64_t rows;            // query tokens: q_offsets[B]
+    int64_t max_rows;        // of one sequence
+    size_t total_bytes;      // workspace
+};
+// q_off: the host copy of the query rows' offsets.
+ts_status_t make_dense_plan(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp);
+cudaError_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, int64_t q_stride_tok,
+                         const int64_t *q_off, void *out, float *lse, uint8_t *ws, cudaStream_t st);
 
 // Token-axis split of one sequence (split.cu): the joins' arithmetic.
 cudaError_t launch_merge_normalisers(const double *L_parts, int parts, int64_t count, double *L_out,

@@ -223,3 +223,74 @@ def test_split_and_comparator_arguments_are_checked_on_the_host(lib):
     assert lib.ts_select_merge(ctypes.byref(one), None, 2, 2, 16, 4, 8, 0, 1000, None, None, None) == 1
     lib.ts_sparse_attn_lse.argtypes = [ctypes.POINTER(_KV), P, P, P, I32, P, P, P, SZ, P]
     assert lib.ts_sparse_attn_lse(ctypes.byref(one), None, None, None, 0, None, None, None, 0, None) == 1
+
+
+def test_new_token_arguments_are_checked_on_the_host(lib):
+    """ts_extend_pages, ts_write_kv and ts_dense_attn refuse bad arguments on
+    the host, before any device query or launch."""
+    lib.ts_last_error.restype = ctypes.c_char_p
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.ts_extend_pages.argtypes = [I32, P, P, I32, P, I64, I64, P, I32, P, P, P, I64, P, P]
+
+    def extend(batch=2, cached=16, fresh=16, page=16, free=16, n_free=4, pool=8, table=16, stride=4, so=16, qo=16,
+               slots=16, n_slots=4, used=16):
+        return lib.ts_extend_pages(batch, cached, fresh, page, free, n_free, pool, table, stride, so, qo, slots, n_slots,
+                                   used, None)
+
+    for bad in ({"batch": 0}, {"n_free": -1}, {"n_slots": -1}, {"pool": 0}, {"stride": 0}, {"cached": None},
+                {"fresh": None}, {"free": None}, {"table": None}, {"so": None}, {"qo": None}, {"slots": None},
+                {"used": None}):
+        assert extend(**bad) == 1, bad
+    for bad, word in (({"batch": 1025}, b"batch"), ({"page": 4}, b"page_size"), ({"page": 24}, b"page_size"),
+                      ({"page": 8192}, b"page_size"), ({"pool": 1 << 27}, b"2^31")):
+        assert extend(**bad) == 2 and word in lib.ts_last_error(), bad
+
+    off = (ctypes.c_int64 * 2)(0, 64)
+    kv = _KV(1, 8, 4, 64, ctypes.addressof(off), ctypes.addressof(off), 16, 32, 256, 64, 0.0)
+    lib.ts_write_kv.argtypes = [ctypes.POINTER(_KV), P, P, P, P, I64, P, I64, P]
+
+    def write(cache=kv, k=16, v=32, k_new=48, v_new=64, st=256, slots=80, n=1):
+        return lib.ts_write_kv(None if cache is None else ctypes.byref(cache), k, v, k_new, v_new, st, slots, n, None)
+
+    for bad, word in (({"cache": None}, b"kv"), ({"k": 48}, b"own"), ({"v": 48}, b"own"), ({"k_new": None}, b"aligned"),
+                      ({"v_new": 8}, b"aligned"), ({"slots": None}, b"slot"), ({"st": 248}, b"stride"),
+                      ({"st": 260}, b"stride"), ({"n": -1}, b"n_new"), ({"n": 1 << 31}, b"n_new")):
+        assert write(**bad) == 1 and word in lib.ts_last_error(), (bad, lib.ts_last_error())
+
+    lib.ts_dense_attn_workspace_bytes.restype = SZ
+    lib.ts_dense_attn_workspace_bytes.argtypes = [ctypes.POINTER(_KV), P]
+    lib.ts_dense_attn.argtypes = [ctypes.POINTER(_KV), P, I64, P, P, P, P, P, SZ, P]
+    q_off = (ctypes.c_int64 * 2)(0, 8)
+    one_behind = (ctypes.c_int64 * 2)(1, 8)
+
+    def attn(cache=kv, q=16, st=512, off_dev=16, off_host=q_off, out=16):
+        return lib.ts_dense_attn(None if cache is None else ctypes.byref(cache), q, st, off_dev,
+                                 None if off_host is None else ctypes.addressof(off_host), out, None, None, 0, None)
+
+    for bad, word in (({"cache": None}, b"kv"), ({"q": 8}, b"aligned"), ({"out": 8}, b"aligned"), ({"st": 504}, b"stride"),
+                      ({"st": 513}, b"stride"), ({"off_host": None}, b"q_offsets_host"),
+                      ({"off_host": one_behind}, b"q_offsets[0]")):
+        assert attn(**bad) == 1 and word in lib.ts_last_error(), (bad, lib.ts_last_error())
+    assert lib.ts_dense_attn_workspace_bytes(ctypes.byref(kv), None) == 0
+    wide = _KV(1, 8, 4, 96, ctypes.addressof(off), ctypes.addressof(off), 16, 32, 384, 96, 0.0)
+    assert attn(cache=wide, st=768) == 2 and b"head_dim" in lib.ts_last_error()
+
+
+def test_binding_refuses_host_tensors_and_wrong_types_of_new_tokens():
+    import torch
+
+    import query_aware_kv_ts_b200 as ts
+    i64 = torch.zeros(1, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU only"):
+        ts.ts_extend_pages(i64, i64, 16, torch.zeros(1, dtype=torch.int32), 1, torch.zeros((1, 1), dtype=torch.int32),
+                           torch.zeros(2, dtype=torch.int64), torch.zeros(2, dtype=torch.int64), i64, i64)
+    dev = torch.device("cpu")
+    rows = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU only"):
+        ts._token_rows("q", rows, 2, 64, dev)
+    with pytest.raises(TypeError, match="torch tensor"):
+        ts._token_rows("q", [1.0], 2, 64, dev)
+    with pytest.raises(ValueError, match="GPU only"):
+        ts._on_device("slots", i64, torch.int64, dev)
+    with pytest.raises(ValueError, match="entries"):
+        ts._host_offsets([0, 1, 2], 1)
