@@ -428,21 +428,40 @@ ts_status_t make_dense_plan(const ts_kv_t *kv, const int64_t *q_off, DensePlan *
     const ts_status_t s = make_plan(kv, -1, &dp->p);
     if (s != TS_OK)
         return s;
-    dp->max_rows = 0;
     for (int b = 0; b < kv->batch; ++b) {
         const int64_t f = q_off[b + 1] - q_off[b];
         if (f < 0) {
             set_error("q_offsets must be non-decreasing (sequence %d)", b);
             return TS_ERR_INVALID_ARG;
         }
-        dp->max_rows = f > dp->max_rows ? f : dp->max_rows;
     }
     dp->rows = q_off[kv->batch];
     if (dp->rows > kMaxDenseRows) {
         set_error("%lld query tokens exceed the supported maximum %lld", (long long)dp->rows, (long long)kMaxDenseRows);
         return TS_ERR_UNSUPPORTED;
     }
-    dp->total_bytes = 256;
+    plan_dense(kv, q_off, dp);
+    return TS_OK;
+}
+
+ts_status_t encode_map3(CUtensorMap *map, const void *base, int64_t channels, int64_t dim1, int64_t dim2,
+                        int64_t stride1, int64_t stride2, int box1, int box2)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) {
+        set_error("cuTensorMapEncodeTiled is not available from the driver");
+        return TS_ERR_CUDA;
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)dim1, (cuuint64_t)dim2};
+    cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride2 * 2};
+    cuuint32_t boxes[3] = {64u, (cuuint32_t)box1, (cuuint32_t)box2}, step[3] = {1u, 1u, 1u};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxes,
+                           step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled failed (%d)", (int)r);
+        return TS_ERR_CUDA;
+    }
     return TS_OK;
 }
 
@@ -1039,9 +1058,8 @@ ts_status_t ts_dense_attn(const ts_kv_t *kv, const void *q, int64_t q_stride_tok
     s = check_ws(dp.total_bytes, ws, ws_bytes);
     if (s != TS_OK)
         return s;
-    const cudaError_t e = launch_dense(dp, kv, q, q_stride_tok, q_offsets, out, lse, static_cast<uint8_t *>(ws),
-                                       static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? TS_OK : cuda_fail(e, "dense attention launch");
+    return launch_dense(dp, kv, q, q_stride_tok, q_offsets, out, lse, static_cast<uint8_t *>(ws),
+                        static_cast<cudaStream_t>(stream));
 }
 
 ts_status_t ts_selftest_expire_wait(void *ws, size_t ws_bytes, uint32_t spin_limit, void *stream)

@@ -1,0 +1,456 @@
+// What the dense attention kernels share: their arguments, and the division
+// of the work over the blocks.
+//
+// An item is a group of up to TT query tokens of one sequence with the G
+// query heads of one kv head, against the tokens that the last of them sees.
+// The items of the whole call stand in one line, sequence by sequence, kv
+// head by kv head, each as long as its tokens plus a constant, and block c
+// takes the c-th of gridDim.x equal parts of that line.  Parts end inside
+// items, at a multiple of kDenseTile tokens; the pieces of such an item are
+// joined by dense_merge.  So blocks are equally loaded at any mixture of
+// lengths, and one long sequence spreads over the whole GPU.  Everything
+// follows from the device's offsets in closed form: no atomics, no order
+// that changes from run to run.
+#pragma once
+
+#include "ts_device.cuh"
+#include "ts_internal.h"
+
+namespace ts {
+
+constexpr int kDenseTile = 128;         // tokens per K / V tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2f = 0.693147180559945309f;
+
+// A block's ends inside items, for dense_merge.
+struct __align__(16) DensePiece {
+    int32_t b, g, t;     // the item that the block begins and does not end
+    int32_t flags;
+};
+enum : int32_t {
+    kPieceHead = 1,      // the block begins an item that it does not end
+    kPieceThrough = 2,   // the block lies wholly inside an item: neither begins nor ends it
+    kPieceEmpty = 4,     // and holds no tile of it
+};
+
+struct DenseArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_st, st, sh;
+    const int64_t *seq_off, *q_off;
+    __nv_bfloat16 *out;
+    float *lse;
+    uint32_t *ctrl;
+    DensePiece *pieces;   // [grid]
+    float *part;          // [2 * grid][rows of an item][D + 4]: weighted V sums, then (max in base 2, sum)
+    int B, Hq, Hkv, G;
+    int TT;               // query tokens per item
+    int single;           // 1: the sequences with one query token, 0: those with more
+    int split;            // 0: parts end between items only
+    float scale, scale_log2;
+    // paged cache (page_table != null): token i of sequence b is pool row
+    // page_table[b * pt_stride + (i >> page_shift)] << page_shift | (i & (page - 1))
+    const int32_t *page_table;
+    int pt_stride, page_shift;
+    int64_t pool_pages;
+};
+
+struct DenseItem {
+    int32_t b, g, t;           // sequence, kv head, group of query tokens
+    int32_t kt0, kt1;          // tiles of this piece, kt0 < kt1 (one empty tile for an item that sees nothing)
+    int32_t tiles;             // of the whole item
+    int32_t tokens;            // query tokens of the item
+    int32_t slot;              // -1: the whole item; else its piece's place in the partial results
+    int64_t q_row;             // its first query row
+    int64_t off, n, first_pos; // the sequence's first row and length; position of its first query token
+};
+
+// Cost of an item beside its tokens, in tokens: measured start and end of an item.
+constexpr int kItemCost = 192;
+
+__device__ __forceinline__ int64_t seq_items(const DenseArgs &a, int64_t f)
+{
+    return (a.single ? f == 1 : f > 1) ? (f + a.TT - 1) / a.TT : 0;
+}
+// Length of the first t items of one kv head of a sequence on the line:
+// item s counts base + (s + 1) TT + kItemCost.
+__device__ __forceinline__ int64_t items_cost(const DenseArgs &a, int64_t base, int64_t t)
+{
+    return t * (base + kItemCost) + (int64_t)a.TT * (t * (t + 1) / 2);
+}
+
+// The line's sequence boundaries in start[0..B] (shared memory).  Every
+// thread of the block calls it.
+__device__ __forceinline__ void dense_line(const DenseArgs &a, int64_t *start, int64_t *s_warp)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
+    int64_t sum = 0;
+    for (int u = 0; u < per; ++u) {
+        const int b = tid * per + u;
+        if (b >= a.B)
+            break;
+        const int64_t n = __ldcg(a.seq_off + b + 1) - __ldcg(a.seq_off + b);
+        const int64_t f = __ldcg(a.q_off + b + 1) - __ldcg(a.q_off + b);
+        sum += a.Hkv * items_cost(a, n > f ? n - f : 0, seq_items(a, f));
+        start[b + 1] = sum;
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += y;
+    }
+    if (lane == 31)
+        s_warp[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - sum;
+    for (int w = 0; w < warp; ++w)
+        before += s_warp[w];
+    for (int u = 0; u < per; ++u) {
+        const int b = tid * per + u;
+        if (b >= a.B)
+            break;
+        start[b + 1] += before;
+    }
+    if (tid == 0)
+        start[0] = 0;
+    __syncthreads();
+}
+
+// A place on the line, at a tile boundary of an item (b == B: its end).
+struct DensePlace {
+    int32_t b, g, t, cut;
+    int32_t tiles;            // of the item
+    int64_t f, n;
+};
+
+__device__ __forceinline__ void dense_item_at(const DenseArgs &a, DensePlace &p)
+{
+    const int64_t last = p.n - p.f + min((int64_t)(p.t + 1) * a.TT, p.f);   // tokens that its last query sees
+    p.tiles = last > 0 ? (int32_t)((last + kDenseTile - 1) / kDenseTile) : 1;
+}
+
+__device__ __forceinline__ void dense_load_seq(const DenseArgs &a, DensePlace &p)
+{
+    p.n = __ldcg(a.seq_off + p.b + 1) - __ldcg(a.seq_off + p.b);
+    p.f = __ldcg(a.q_off + p.b + 1) - __ldcg(a.q_off + p.b);
+}
+
+__device__ __forceinline__ void dense_next_item(const DenseArgs &a, const int64_t *start, DensePlace &p)
+{
+    p.cut = 0;
+    if (++p.t >= seq_items(a, p.f)) {
+        p.t = 0;
+        if (++p.g == a.Hkv) {
+            p.g = 0;
+            do {
+                ++p.b;
+            } while (p.b < a.B && start[p.b + 1] == start[p.b]);
+            if (p.b < a.B)
+                dense_load_seq(a, p);
+        }
+    }
+    if (p.b < a.B)
+        dense_item_at(a, p);
+}
+
+__device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int64_t *start, int64_t x)
+{
+    DensePlace p;
+    p.b = a.B;
+    p.g = p.t = p.cut = p.tiles = 0;
+    p.f = p.n = 0;
+    if (x >= start[a.B])
+        return p;
+    int lo = 0, hi = a.B;                      // start[lo] <= x < start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    p.b = lo;
+    dense_load_seq(a, p);
+    const int64_t base = p.n > p.f ? p.n - p.f : 0, items = seq_items(a, p.f);
+    const int64_t head = items_cost(a, base, items);
+    int64_t rem = x - start[lo];
+    p.g = (int32_t)(rem / head);
+    rem -= p.g * head;
+    int64_t t0 = 0, t1 = items;                // items_cost(t0) <= rem < items_cost(t1)
+    while (t1 - t0 > 1) {
+        const int64_t mid = (t0 + t1) >> 1;
+        if (items_cost(a, base, mid) <= rem)
+            t0 = mid;
+        else
+            t1 = mid;
+    }
+    p.t = (int32_t)t0;
+    rem -= items_cost(a, base, t0);
+    dense_item_at(a, p);
+    if (a.split) {
+        const int64_t c = (rem - kItemCost + kDenseTile / 2) / kDenseTile;
+        p.cut = (int32_t)(c < 0 ? 0 : (c < p.tiles ? c : p.tiles));
+        if (p.tiles >= 8) {                    // no piece of a single tile
+            if (p.cut < 2)
+                p.cut = 0;
+            else if (p.cut > p.tiles - 2)
+                p.cut = p.tiles;
+        }
+    } else {
+        p.cut = 2 * rem < base + (t0 + 1) * a.TT + kItemCost ? 0 : p.tiles;
+    }
+    if (p.cut == p.tiles)
+        dense_next_item(a, start, p);
+    return p;
+}
+
+// The pieces of block c, one after another: next() is false at the end of
+// its part.  One thread walks (or all of a warp alike).
+struct DenseWalk {
+    DensePlace at, end;
+
+    __device__ __forceinline__ void begin(const DenseArgs &a, const int64_t *start)
+    {
+        const int64_t total = start[a.B], c = blockIdx.x, n = gridDim.x;
+        at = dense_locate(a, start, total / n * c + total % n * c / n);
+        end = dense_locate(a, start, total / n * (c + 1) + total % n * (c + 1) / n);
+    }
+    __device__ __forceinline__ bool same_item() const { return at.b == end.b && at.g == end.g && at.t == end.t; }
+    // For dense_merge; call it before next().
+    __device__ __forceinline__ DensePiece piece(const DenseArgs &a) const
+    {
+        DensePiece p;
+        p.b = end.b;
+        p.g = end.g;
+        p.t = end.t;
+        const bool inside = end.b < a.B && end.cut > 0;     // the part ends inside an item
+        p.flags = inside ? (same_item() && at.cut > 0 ? kPieceThrough : kPieceHead) : 0;
+        if (inside && same_item() && at.cut == end.cut)
+            p.flags = kPieceThrough | kPieceEmpty;
+        return p;
+    }
+    __device__ __forceinline__ bool next(const DenseArgs &a, const int64_t *start, DenseItem &it)
+    {
+        if (at.b >= a.B)
+            return false;
+        const bool last = same_item();
+        if (last && at.cut >= end.cut)
+            return false;
+        it.b = at.b;
+        it.g = at.g;
+        it.t = at.t;
+        it.kt0 = at.cut;
+        it.kt1 = last ? end.cut : at.tiles;
+        it.tiles = at.tiles;
+        it.tokens = (int32_t)min((int64_t)a.TT, at.f - (int64_t)at.t * a.TT);
+        it.slot = it.kt0 == 0 && it.kt1 == at.tiles ? -1 : 2 * (int32_t)blockIdx.x + (it.kt0 == 0 ? 1 : 0);
+        it.off = __ldcg(a.seq_off + at.b);
+        it.q_row = __ldcg(a.q_off + at.b) + (int64_t)at.t * a.TT;
+        it.n = at.n;
+        it.first_pos = at.n - at.f + (int64_t)at.t * a.TT;
+        if (last)
+            at.cut = end.cut;                                // next() ends here
+        else
+            dense_next_item(a, start, at);
+        return true;
+    }
+};
+
+// The K / V row of token i < n of a sequence; -1 on a page outside the pool.
+__device__ __forceinline__ int64_t dense_row(const DenseArgs &a, int b, int64_t off, int64_t i)
+{
+    if (a.page_table == nullptr)
+        return off + i;
+    const int32_t pg = __ldcg(a.page_table + (int64_t)b * a.pt_stride + (i >> a.page_shift));
+    if (pg < 0 || pg >= a.pool_pages)
+        return -1;
+    return ((int64_t)pg << a.page_shift) + (i & (((int64_t)1 << a.page_shift) - 1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+// The two bf16 of w with infinities and NaN replaced by zero.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w)
+{
+    if ((w & 0x7f80u) == 0x7f80u)
+        w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u)
+        w &= 0x0000ffffu;
+    return w;
+}
+
+// First tile of an item in which some token is not seen by all its queries:
+// there V may hold what no weight of zero takes away (inf, NaN), and rows
+// that no token owns.
+__device__ __forceinline__ int64_t dense_masked_from(int64_t first_pos)
+{
+    return first_pos + 1 > 0 ? (first_pos + 1) / kDenseTile : 0;
+}
+
+constexpr int kStreamRows = 128;            // packed rows of one accumulator: floor(128 / G) tokens x G heads
+constexpr int kItemSlots = 4;
+template <int D>
+constexpr int kTileBytes = kDenseTile * D * 2;
+
+// What the loading warp and the others of a block share: a ring of K and V
+// tiles and a ring of items.
+template <int NS>
+struct DenseRing {
+    uint64_t full[NS], empty[NS];
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+    DenseItem item[kItemSlots];
+
+    // arrivals that free an even stage, an odd one, an item
+    __device__ void init(int stages, int even_readers, int odd_readers, int item_readers)
+    {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], s & 1 ? odd_readers : even_readers);
+        }
+        for (int s = 0; s < kItemSlots; ++s) {
+            mbar_init(&item_full[s], 1);
+            mbar_init(&item_empty[s], item_readers);
+        }
+    }
+};
+
+template <int D>
+struct QueryLoad {
+    const CUtensorMap *map;
+    uint8_t *sq;                             // two streams of 128 rows
+    uint64_t *full, *empty;
+    int32_t *bad;                            // per item slot, cleared when an item begins
+};
+
+__device__ __forceinline__ void tma_load_tile(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
+                                              int32_t z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Whole warp: wait for a barrier's phase, bounded; false when it gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *ctrl, int lane)
+{
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kSpinLimit));
+    if (!ok && lane == 0)
+        report_timeout(ctrl, kSiteDense);
+    return ok;
+}
+
+// The loading warp: walks the block's items, publishes each, and streams its
+// K and V tiles (K and V of a tile in turn; 64-channel halves of 128-byte
+// rows, 128-byte swizzle) into the ring, and with QL its queries.  A tile is
+// one box {64 channels, 128 tokens, 1 head} per half, or in a paged cache with
+// shorter pages one box per page and half, each issued by its own lane.  An
+// item with b < 0 ends the line.
+template <int D, int NS, bool QL, int MAXNS>
+__device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> &r, const int64_t *start,
+                                           uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap, int box,
+                                           int lane, const QueryLoad<D> &q)
+{
+    const int T = kStreamRows / a.G;
+    const int npp = kDenseTile / box;                // boxes along a tile's tokens
+    const int p = lane % npp, half = lane / npp;     // this lane's box: page p of the tile, 64 channels
+    const bool mine = lane < npp * (D / 64);
+    const int64_t oob = a.pool_pages << a.page_shift;   // past the pool: reads zeros
+    DenseWalk w;
+    w.begin(a, start);
+    if (lane == 0)
+        a.pieces[blockIdx.x] = w.piece(a);
+    uint32_t n = 0;                                  // tiles loaded (K and V count one each)
+    DenseItem it;
+    bool ok = true;
+    uint32_t k = 0;
+    for (; ok; ++k) {
+        const bool more = w.next(a, start, it);
+        const int slot = k % kItemSlots;
+        if (k >= kItemSlots && !warp_wait(&r.item_empty[slot], ((k / kItemSlots) - 1) & 1, a.ctrl, lane)) {
+            ok = false;
+            break;
+        }
+        if (lane == 0) {
+            if (!more)
+                it.b = -1;
+            r.item[slot] = it;
+            if (QL)
+                q.bad[slot] = 0;
+            mbar_arrive(&r.item_full[slot]);
+        }
+        if (!more)
+            break;
+        if (QL) {
+            if (k > 0 && !warp_wait(q.empty, (k - 1) & 1, a.ctrl, lane)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                const int streams = it.tokens > T ? 2 : 1;
+                mbar_arrive_expect_tx(q.full, (uint32_t)(streams * T * a.G * D * 2));
+                for (int s = 0; s < streams; ++s)
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_tile(q.sq + (s * (D / 64) + x) * (kStreamRows * 128), q.map, q.full, x * 64,
+                                      it.g * a.G, (int32_t)(it.q_row + s * T));
+            }
+        }
+        int32_t row = 0;
+        for (int kt = it.kt0; kt < it.kt1 && ok; ++kt) {
+            const int ahead = (kt - it.kt0) % (32 / npp);
+            int32_t y;
+            if (a.page_table == nullptr) {
+                y = (int32_t)(it.off + (int64_t)kt * kDenseTile);
+            } else {
+                if (ahead == 0) {
+                    // one round trip to the block table finds the pages of the
+                    // next 32 / npp tiles, one page a lane
+                    const int64_t i = (int64_t)(kt + lane / npp) * kDenseTile + (int64_t)p * box;
+                    const int64_t found = i < it.n ? dense_row(a, it.b, it.off, i) : -1;
+                    row = (int32_t)(found < 0 ? oob : found);
+                }
+                y = __shfl_sync(0xffffffffu, row, ahead * npp + p);
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int st = n % NS;
+                if (n >= (uint32_t)NS && !warp_wait(&r.empty[st], ((n / NS) - 1) & 1, a.ctrl, lane)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&r.full[st], (uint32_t)kTileBytes<D>);
+                __syncwarp();
+                if (mine)
+                    tma_load_tile(ring + st * kTileBytes<D> + half * (kDenseTile * 128) + p * box * 128,
+                                  kv ? vmap : kmap, &r.full[st], half * 64, y, it.g);
+                ++n;
+            }
+        }
+    }
+    // a wait gave up: no more loads are issued; wait (bounded) for those in
+    // flight, the last NS tiles and the queries, before the block may end
+    if (!ok) {
+        for (uint32_t j = n > (uint32_t)NS ? n - NS : 0u; j < n; ++j)
+            (void)mbar_wait_bounded(&r.full[j % NS], (j / NS) & 1, kSpinLimit);
+        if (QL && k > 0)
+            (void)mbar_wait_bounded(q.full, (k - 1) & 1, kSpinLimit);
+    }
+}
+
+}  // namespace ts

@@ -1,0 +1,492 @@
+// Dense attention on the 5th-generation tensor cores: sequences with two or
+// more query tokens (whole prompts, chunks).  For an item (see
+// dense_common.cuh) of query tokens x the G heads of a kv head:
+//   S = Q K^T            [128 x 128] per tile of 128 tokens, fp32 in TMEM
+//   m, l                 running maximum and sum of each row
+//   P = 2^((S - m) c)    rounded to bf16, written over S in TMEM (c = scale log2 e)
+//   O += P V             [128 x d], fp32 in TMEM
+//
+// One persistent block per SM.  Two streams of 128 packed rows each (T =
+// floor(128 / G) tokens x G heads, token-major: one row of the accumulator is
+// one thread) share every K and V tile.  Warps 0-3 and 4-7 are the streams'
+// softmax, one thread a row, so that no reduction crosses threads; warp 8
+// walks the items and loads Q, K and V with TMA (128-byte swizzle) into a
+// ring of tiles; warp 9 issues the MMAs; warp 10 clears what a masked token
+// must not leak out of V.  While one stream's softmax runs, the tensor cores
+// do the other's products.
+//
+// The maximum is only raised when a row's new one is 2^8 above the old (the
+// weights then stay below 2^8, far from fp32's limits, and the result is
+// divided by a sum with the same reference), so O is rarely rescaled.
+#include "dense_common.cuh"
+
+namespace ts {
+namespace {
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;   // 10: the V guard
+constexpr int kTcThreads = 11 * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;            // S (and P over it) at 0 and 128, O at 256 and 256 + d
+constexpr float kRaise = 8.0f;              // log2 of how far weights may grow before O is rescaled
+
+constexpr int kTcRingBytes = 128 * 1024;    // K / V tiles
+template <int D>
+constexpr int kStages = kTcRingBytes / kTileBytes<D>;   // even: K and V take turns
+
+struct TcShared {
+    DenseRing<8> ring;
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_ready[2], o_full[2];
+    uint64_t clean[8];                       // the masked V tile in this stage has been cleared
+    uint64_t done;
+    int32_t bad[kItemSlots];                 // the item's masked tiles held infinities or NaN in V
+    uint32_t tmem;
+    int64_t s_warp[kTcThreads / 32];
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], B stored with its N index contiguous.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Shared-memory descriptor of an operand whose M / N index is contiguous:
+// 64-channel blocks of 128-byte rows (one row a token), 128-byte swizzle.
+// 8 tokens are 1024 bytes apart (stride), 64-channel blocks block_bytes
+// (leading dimension).
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t smem_addr, uint32_t block_bytes)
+{
+    return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)(block_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+            v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- the softmax of one stream: 128 threads, one row each ------------------
+template <int D>
+__device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh, int stream, int quarter, int lane)
+{
+    const int r = quarter * 32 + lane;               // the row in the stream
+    const int T = kStreamRows / a.G;
+    const uint32_t lanes = sh.tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ts = lanes + stream * 128, to = lanes + kTmemO + stream * D;
+    const int token = r / a.G, head = r - token * a.G;
+    const float c = a.scale_log2;
+    uint32_t phase = 0, done = 0;                    // of s_full and o_full
+    for (uint32_t k = 0;; ++k) {
+        if (!warp_wait(&sh.ring.item_full[k % kItemSlots], (k / kItemSlots) & 1, a.ctrl, lane))
+            return;
+        const DenseItem it = sh.ring.item[k % kItemSlots];
+        if (it.b < 0)
+            return;
+        const int tokens = min(T, it.tokens - stream * T);
+        if (tokens <= 0) {                           // the item fills the first stream only
+            if (lane == 0)
+                mbar_arrive(&sh.ring.item_empty[k % kItemSlots]);
+            continue;
+        }
+        const int64_t pos = it.first_pos + stream * T + token;
+        const int64_t masked_from = dense_masked_from(it.first_pos);
+        float m = -INFINITY, l = 0.0f;               // m in units of S
+        for (int kt = it.kt0; kt < it.kt1; ++kt) {
+            if (!warp_wait(&sh.s_full[stream], phase & 1, a.ctrl, lane))
+                return;
+            ++phase;
+            tmem_fence_after();
+            float s[kDenseTile];
+#pragma unroll
+            for (int x = 0; x < kDenseTile / 32; ++x)
+                tmem_ld32(ts + x * 32, reinterpret_cast<uint32_t *>(s) + x * 32);
+            tmem_wait_ld();
+            if (kt >= masked_from) {
+                const int64_t left = pos + 1 - (int64_t)kt * kDenseTile;
+                const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
+                // behind the limit: the end of the scale's range that weighs nothing
+                const float none = c < 0.0f ? INFINITY : -INFINITY;
+#pragma unroll
+                for (int x = 0; x < kDenseTile; ++x)
+                    s[x] = x < limit ? s[x] : none;
+            }
+            float mx[4];
+            if (c < 0.0f) {
+#pragma unroll
+                for (int x = 0; x < kDenseTile; ++x)
+                    s[x] = -s[x];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                mx[u] = s[u];
+#pragma unroll
+            for (int x = 4; x < kDenseTile; ++x)
+                mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float ca = fabsf(c);
+            bool raise = (top - m) * ca > kRaise;    // (the first tile that a row sees anything of, too)
+            if (kt == it.kt0) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, raise)) {
+                float f = 1.0f;
+                if (raise) {
+                    f = ex2((m - top) * ca);
+                    m = top;
+                }
+                l *= f;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t o[32];
+                    tmem_ld32(to + x * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st32(to + x * 32, o);
+                }
+            }
+            const float mc = m == -INFINITY ? 0.0f : m * ca;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x = 0; x < kDenseTile / 32; ++x) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = ex2(fmaf(s[x * 32 + e], ca, -mc)), p1 = ex2(fmaf(s[x * 32 + e + 1], ca, -mc));
+                    sum[e & 2] += p0;
+                    sum[(e & 2) + 1] += p1;
+                    p[e / 2] = pack_bf16(p0, p1);
+                }
+                tmem_st16(ts + x * 16, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.p_ready[stream]);
+        }
+        // the item's end: O / l to the output, or O, m and l to the partial results
+        if (!warp_wait(&sh.o_full[stream], done & 1, a.ctrl, lane))
+            return;
+        ++done;
+        tmem_fence_after();
+        const bool live = token < tokens, whole = it.slot < 0;
+        const bool bad = sh.bad[k % kItemSlots] != 0;
+        const int64_t row = (it.q_row + stream * T + token) * a.Hq + it.g * a.G + head;
+        float *part = a.part + ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + r) * (D + 4);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld32(to + x * 32, o);
+            tmem_wait_ld();
+            if (live && bad) {
+                // infinities and NaN of the masked tiles that this row sees
+                const int64_t t0 = max(masked_from, (int64_t)it.kt0) * kDenseTile;
+                const int64_t t1 = min(pos + 1, (int64_t)it.kt1 * kDenseTile);
+                for (int64_t t = t0; t < t1; ++t) {
+                    const int64_t vr = dense_row(a, it.b, it.off, t);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float y = vr < 0 ? 0.0f : __bfloat162float(a.v[vr * a.st + it.g * a.sh + x * 32 + e]);
+                        if (!isfinite(y))
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+                    }
+                }
+            }
+            if (live && whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 w;
+                    w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                    w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                    w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                    *reinterpret_cast<uint4 *>(a.out + row * D + x * 32 + e) = w;
+                }
+            } else if (live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4 *>(part + x * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+            __syncwarp();
+        }
+        if (live) {
+            const float mb = m * fabsf(c);
+            if (!whole)
+                *reinterpret_cast<float2 *>(part + D) = make_float2(mb, l);
+            else if (a.lse != nullptr)
+                a.lse[row] = l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.ring.item_empty[k % kItemSlots]);
+    }
+}
+
+// ---- the products, issued by one thread -------------------------------------
+template <int D>
+__device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh, uint32_t sq, uint32_t ring)
+{
+    constexpr int NS = kStages<D>;
+    constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, kDenseTile);
+    constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | (1u << 16);   // B's N index is contiguous
+    const int T = kStreamRows / a.G;
+    const uint32_t tmem = sh.tmem;
+    uint32_t n = 0;                                  // tiles consumed
+    uint32_t p_phase[2] = {0, 0}, clean = 0;
+    auto fail = [&]() { report_timeout(a.ctrl, kSiteDense); };
+    auto scores = [&](int s, int st) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (uint32_t)((ks >> 2) * (128 * 128) + (ks & 3) * 32);
+            umma_bf16(tmem + s * 128, umma_desc_sw128(sq + s * (kStreamRows * D * 2) + off),
+                      umma_desc_sw128(ring + st * kTileBytes<D> + off), idesc_s, ks > 0);
+        }
+        umma_commit(&sh.s_full[s]);
+    };
+    for (uint32_t k = 0;; ++k) {
+        if (!mbar_wait_bounded(&sh.ring.item_full[k % kItemSlots], (k / kItemSlots) & 1, kSpinLimit))
+            return fail();
+        const int32_t b = sh.ring.item[k % kItemSlots].b;
+        if (b < 0)
+            return;
+        const int kt0 = sh.ring.item[k % kItemSlots].kt0, kt1 = sh.ring.item[k % kItemSlots].kt1;
+        const int streams = sh.ring.item[k % kItemSlots].tokens > T ? 2 : 1;
+        const int64_t masked_from = dense_masked_from(sh.ring.item[k % kItemSlots].first_pos);
+        if (!mbar_wait_bounded(&sh.q_full, k & 1, kSpinLimit))
+            return fail();
+        {
+            const int st = n % NS;
+            if (!mbar_wait_bounded(&sh.ring.full[st], (n / NS) & 1, kSpinLimit))
+                return fail();
+            tmem_fence_after();
+            for (int s = 0; s < streams; ++s)
+                scores(s, st);
+            umma_commit(&sh.ring.empty[st]);
+            if (kt0 + 1 == kt1)
+                umma_commit(&sh.q_empty);
+            ++n;
+        }
+        for (int kt = kt0; kt < kt1; ++kt) {
+            const int sv = n % NS, sk = (n + 1) % NS;
+            const bool more = kt + 1 < kt1;
+            bool ok;
+            if (kt >= masked_from) {
+                ok = mbar_wait_bounded(&sh.clean[sv], (clean >> sv) & 1, kSpinLimit);
+                clean ^= 1u << sv;
+            } else {
+                ok = mbar_wait_bounded(&sh.ring.full[sv], (n / NS) & 1, kSpinLimit);
+            }
+            if (!ok)
+                return fail();
+            for (int s = 0; s < streams; ++s) {
+                if (!mbar_wait_bounded(&sh.p_ready[s], p_phase[s] & 1, kSpinLimit))
+                    return fail();
+                ++p_phase[s];
+                tmem_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < kDenseTile / 16; ++ks)
+                    umma_bf16_ts(tmem + kTmemO + s * D, tmem + s * 128 + ks * 8,
+                                 umma_desc_sw128_mn(ring + sv * kTileBytes<D> + ks * 2048, kDenseTile * 128), idesc_o,
+                                 kt > kt0 || ks > 0);
+                if (s + 1 == streams)
+                    umma_commit(&sh.ring.empty[sv]);
+                if (!more) {
+                    umma_commit(&sh.o_full[s]);
+                    continue;
+                }
+                if (s == 0 && !mbar_wait_bounded(&sh.ring.full[sk], ((n + 1) / NS) & 1, kSpinLimit))
+                    return fail();
+                tmem_fence_after();
+                scores(s, sk);
+                if (s + 1 == streams) {
+                    umma_commit(&sh.ring.empty[sk]);
+                    if (kt + 2 == kt1)
+                        umma_commit(&sh.q_empty);
+                }
+            }
+            n += more ? 2 : 1;
+        }
+        mbar_arrive(&sh.ring.item_empty[k % kItemSlots]);
+    }
+}
+
+// ---- V of the masked tiles ---------------------------------------------------
+// A masked token's weight is 0, but 0 times an infinity or NaN is NaN in the
+// product.  So in tiles that some row does not see whole, rows behind the
+// sequence's end become zero, and so do infinite and NaN elements, which the
+// softmax threads add to the rows that do see them.
+template <int D>
+__device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, uint8_t *ring, int lane)
+{
+    constexpr int NS = kStages<D>;
+    uint32_t n = 0;
+    for (uint32_t k = 0;; ++k) {
+        const int slot = k % kItemSlots;
+        if (!warp_wait(&sh.ring.item_full[slot], (k / kItemSlots) & 1, a.ctrl, lane))
+            return;
+        if (sh.ring.item[slot].b < 0)
+            return;
+        const int kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
+        const int64_t end = sh.ring.item[slot].n, masked_from = dense_masked_from(sh.ring.item[slot].first_pos);
+        for (int kt = kt0; kt < kt1; ++kt, n += 2) {
+            // it waits for and releases every V tile, so that it never falls a
+            // turn of the ring behind or ahead of the barriers' phases
+            const int st = (n + 1) % NS;
+            if (!warp_wait(&sh.ring.full[st], ((n + 1) / NS) & 1, a.ctrl, lane))
+                return;
+            if (kt < masked_from) {
+                if (lane == 0)
+                    mbar_arrive(&sh.ring.empty[st]);
+                continue;
+            }
+            uint4 *tile = reinterpret_cast<uint4 *>(ring + st * kTileBytes<D>);
+            const int64_t left = end - (int64_t)kt * kDenseTile;
+            bool bad = false;
+#pragma unroll 8
+            for (int i = lane; i < kTileBytes<D> / 16; i += 32) {
+                const bool own = ((i >> 3) & (kDenseTile - 1)) < left;   // 8 pieces a token's 128-byte row
+                const uint4 x = tile[i];
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (own)
+                    w = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+                if (w.x != x.x || w.y != x.y || w.z != x.z || w.w != x.w) {
+                    tile[i] = w;
+                    bad |= own;
+                }
+            }
+            if (bad)
+                sh.bad[slot] = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.clean[st]);
+                mbar_arrive(&sh.ring.empty[st]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.ring.item_empty[slot]);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DenseArgs a, int box)
+{
+    extern __shared__ uint8_t dyn_smem[];
+    __shared__ TcShared sh;
+    uint8_t *sq = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = sq + 2 * kStreamRows * D * 2;
+    int64_t *start = reinterpret_cast<int64_t *>(ring + kStages<D> * kTileBytes<D>);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        // K tiles have the even stages, read by the MMAs; V tiles the odd
+        // ones, read by the MMAs and the guard
+        sh.ring.init(kStages<D>, 1, 2, kSoftmaxWarps + 2);
+        for (int s = 0; s < kStages<D>; ++s)
+            mbar_init(&sh.clean[s], 1);
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh.s_full[s], 1);
+            mbar_init(&sh.p_ready[s], 4);
+            mbar_init(&sh.o_full[s], 1);
+        }
+        mbar_init(&sh.done, 1);
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp)
+        tmem_alloc(&sh.tmem, kTmemCols);
+    if (warp == kLoadWarp && lane < 3)
+        tma_prefetch_desc(lane == 0 ? &qmap : (lane == 1 ? &kmap : &vmap));
+    pdl_wait();
+    pdl_launch_dependents();
+    tmem_fence_before();
+    dense_line(a, start, sh.s_warp);                 // ends with a barrier
+    tmem_fence_after();
+
+    if (warp < kSoftmaxWarps) {
+        softmax_stream<D>(a, sh, warp >> 2, warp & 3, lane);
+    } else if (warp == kLoadWarp) {
+        const QueryLoad<D> q = {&qmap, sq, &sh.q_full, &sh.q_empty, sh.bad};
+        load_items<D, kStages<D>, true>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, q);
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            issue_products<D>(a, sh, smem_u32(sq), smem_u32(ring));
+            // every MMA issued has completed before TMEM is released
+            umma_commit(&sh.done);
+            if (!mbar_wait_bounded(&sh.done, 0, kSpinLimit)) {
+                report_timeout(a.ctrl, kSiteDense);
+                (void)mbar_wait_bounded(&sh.done, 0, kSpinLimit);
+            }
+        }
+        __syncwarp();
+    } else {
+        guard_values<D>(a, sh, ring, lane);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kMmaWarp)
+        tmem_dealloc(sh.tmem, kTmemCols);
+}
+
+}  // namespace
+
+size_t dense_tc_smem(int D, int B)
+{
+    return 1024 + (size_t)2 * kStreamRows * D * 2 + kTcRingBytes + (size_t)(B + 1) * 8;
+}
+
+cudaError_t launch_dense_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                            const DenseArgs &a, int D, int box, int grid, cudaStream_t st)
+{
+    const size_t smem = dense_tc_smem(D, a.B);
+    const void *kernel = D == 128 ? (const void *)dense_tc<128> : (const void *)dense_tc<64>;
+    const cudaError_t e = ensure_dyn_smem(kernel, (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    return D == 128 ? launch_ex(dense_tc<128>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a, box)
+                    : launch_ex(dense_tc<64>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a, box);
+}
+
+}  // namespace ts

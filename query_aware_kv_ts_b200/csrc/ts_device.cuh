@@ -23,6 +23,7 @@ enum : uint32_t {
     kSiteScoreMma = 5,        // score MMA issuer waiting for a stage, a free accumulator or its own MMAs
     kSiteFusedGrid = 6,       // fused scoring waiting for every CTA to finish a pass
     kSiteFusedCta = 7,        // fused scoring: a warp waiting for the other vote workers of its CTA
+    kSiteDense = 8,           // dense attention waiting for a tile, an accumulator or an item
     kSiteSelftest = 99,
 };
 

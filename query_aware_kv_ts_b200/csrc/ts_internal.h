@@ -226,16 +226,29 @@ cudaError_t launch_write_kv(const Plan &p, const ts_kv_t *kv, void *k_cache, voi
                             cudaStream_t st);
 
 // Attention of the newest tokens over the whole cache (dense.cu).
+struct DenseLaunch {
+    int TT;                  // query tokens per item
+    int grid;                // blocks (0: no sequence of this kind)
+    int split;               // items may be cut between blocks
+    int slot_rows;           // rows of one partial result
+    size_t off_pieces, off_part;
+};
 struct DensePlan {
     Plan p;
     int64_t rows;            // query tokens: q_offsets[B]
-    int64_t max_rows;        // of one sequence
+    DenseLaunch launch[2];   // [0] sequences of several query tokens, [1] of one
     size_t total_bytes;      // workspace
 };
 // q_off: the host copy of the query rows' offsets.
 ts_status_t make_dense_plan(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp);
-cudaError_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, int64_t q_stride_tok,
+void plan_dense(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp);   // fills launch and total_bytes
+ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, int64_t q_stride_tok,
                          const int64_t *q_off, void *out, float *lse, uint8_t *ws, cudaStream_t st);
+
+// A bf16 tensor [dim2][dim1][channels] (strides in elements) in TMA boxes
+// {64 channels, box1, box2} with the 128-byte swizzle; zeros outside it.
+ts_status_t encode_map3(CUtensorMap *map, const void *base, int64_t channels, int64_t dim1, int64_t dim2,
+                        int64_t stride1, int64_t stride2, int box1, int box2);
 
 // Token-axis split of one sequence (split.cu): the joins' arithmetic.
 cudaError_t launch_merge_normalisers(const double *L_parts, int parts, int64_t count, double *L_out,
