@@ -24,8 +24,12 @@ namespace ts {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;   // 10: the V guard
-constexpr int kTcThreads = 11 * 32;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;   // and an idle one
+constexpr int kTcThreads = 12 * 32;
+// Registers: 384 threads x 168 at launch; the loading, issuing and guarding
+// warps' group gives up some, the two softmax groups take them
+// (128 x 96 + 256 x 200 <= 384 x 168).
+constexpr int kAuxRegs = 96, kSoftmaxRegs = 200;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;            // S (and P over it) at 0 and 128, O at 256 and 256 + d
 constexpr float kRaise = 8.0f;              // log2 of how far weights may grow before O is rescaled
@@ -99,33 +103,131 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 operations of one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// O of this row times f.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t to, float f)
+{
+#pragma unroll 1
+    for (int x = 0; x < D / 16; ++x) {
+        uint32_t o[16];
+        tmem_ld_32x32b<16>(to + x * 16, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st16(to + x * 16, o);
+    }
+}
+
+// The item's end for this thread's row: O / l to the output, or O, m and l to
+// the partial results.  mb: the row's reference in base 2.
+template <int D>
+__device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &it, bool bad, int stream, int r,
+                                           uint32_t to, float mb, float l)
+{
+    const int T = kStreamRows / a.G;
+    const int token = r / a.G, head = r - token * a.G;
+    const bool live = token < min(T, it.tokens - stream * T), whole = it.slot < 0;
+    const int64_t row = (it.q_row + stream * T + token) * a.Hq + it.g * a.G + head;
+    float *part = a.part + ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + r) * (D + 4);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+    for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        tmem_ld32(to + x * 32, o);
+        tmem_wait_ld();
+        if (live && bad) {
+            // infinities and NaN of the masked tiles that this row sees
+            const int64_t pos = it.first_pos + stream * T + token;
+            const int64_t t0 = max(it.first_pos + 1, (int64_t)it.kt0 * kDenseTile);
+            const int64_t t1 = min(pos + 1, (int64_t)it.kt1 * kDenseTile);
+            for (int64_t t = t0; t < t1; ++t) {
+                const int64_t vr = dense_row(a, it.b, it.off, t);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float y = vr < 0 ? 0.0f : __bfloat162float(a.v[vr * a.st + it.g * a.sh + x * 32 + e]);
+                    if (!isfinite(y))
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+                }
+            }
+        }
+        if (live && whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint4 w;
+                w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                *reinterpret_cast<uint4 *>(a.out + row * D + x * 32 + e) = w;
+            }
+        } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4 *>(part + x * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        __syncwarp();
+    }
+    if (live) {
+        if (!whole)
+            *reinterpret_cast<float2 *>(part + D) = make_float2(mb, l);
+        else if (a.lse != nullptr)
+            a.lse[row] = l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
+    }
+}
+
 // ---- the softmax of one stream: 128 threads, one row each ------------------
 template <int D>
 __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh, int stream, int quarter, int lane)
 {
     const int r = quarter * 32 + lane;               // the row in the stream
-    const int T = kStreamRows / a.G;
     const uint32_t lanes = sh.tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t ts = lanes + stream * 128, to = lanes + kTmemO + stream * D;
-    const int token = r / a.G, head = r - token * a.G;
-    const float c = a.scale_log2;
+    const bool negative = a.scale_log2 < 0.0f;
+    const float c = fabsf(a.scale_log2);
     uint32_t phase = 0, done = 0;                    // of s_full and o_full
     for (uint32_t k = 0;; ++k) {
-        if (!warp_wait(&sh.ring.item_full[k % kItemSlots], (k / kItemSlots) & 1, a.ctrl, lane))
+        const int slot = k % kItemSlots;
+        if (!warp_wait(&sh.ring.item_full[slot], (k / kItemSlots) & 1, a.ctrl, lane))
             return;
-        const DenseItem it = sh.ring.item[k % kItemSlots];
-        if (it.b < 0)
+        if (sh.ring.item[slot].b < 0)
             return;
-        const int tokens = min(T, it.tokens - stream * T);
-        if (tokens <= 0) {                           // the item fills the first stream only
+        const int first = stream * (kStreamRows / a.G);   // of the stream's tokens in the item
+        if (first >= sh.ring.item[slot].tokens) {    // the item fills the first stream only
             if (lane == 0)
-                mbar_arrive(&sh.ring.item_empty[k % kItemSlots]);
+                mbar_arrive(&sh.ring.item_empty[slot]);
             continue;
         }
-        const int64_t pos = it.first_pos + stream * T + token;
-        const int64_t masked_from = dense_masked_from(it.first_pos);
+        const int kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
+        const int masked_from = (int)dense_masked_from(sh.ring.item[slot].first_pos);
+        // tokens that this row sees from tile kt0 on
+        int64_t left = sh.ring.item[slot].first_pos + first + r / a.G + 1 - (int64_t)kt0 * kDenseTile;
         float m = -INFINITY, l = 0.0f;               // m in units of S
-        for (int kt = it.kt0; kt < it.kt1; ++kt) {
+        for (int kt = kt0; kt < kt1; ++kt, left -= kDenseTile) {
             if (!warp_wait(&sh.s_full[stream], phase & 1, a.ctrl, lane))
                 return;
             ++phase;
@@ -135,224 +237,211 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
             for (int x = 0; x < kDenseTile / 32; ++x)
                 tmem_ld32(ts + x * 32, reinterpret_cast<uint32_t *>(s) + x * 32);
             tmem_wait_ld();
-            if (kt >= masked_from) {
-                const int64_t left = pos + 1 - (int64_t)kt * kDenseTile;
-                const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
-                // behind the limit: the end of the scale's range that weighs nothing
-                const float none = c < 0.0f ? INFINITY : -INFINITY;
-#pragma unroll
-                for (int x = 0; x < kDenseTile; ++x)
-                    s[x] = x < limit ? s[x] : none;
-            }
-            float mx[4];
-            if (c < 0.0f) {
+            if (negative) {
 #pragma unroll
                 for (int x = 0; x < kDenseTile; ++x)
                     s[x] = -s[x];
             }
+            if (kt >= masked_from) {
+                const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
+#pragma unroll
+                for (int x = 0; x < kDenseTile; ++x)
+                    s[x] = x < limit ? s[x] : -INFINITY;
+            }
+            float mx[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                mx[u] = s[u];
+                mx[u] = fmaxf(s[u], s[u + 4]);
 #pragma unroll
-            for (int x = 4; x < kDenseTile; ++x)
-                mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+            for (int x = 8; x < kDenseTile; x += 8)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    mx[u] = fmaxf(mx[u], fmaxf(s[x + u], s[x + u + 4]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const float ca = fabsf(c);
-            bool raise = (top - m) * ca > kRaise;    // (the first tile that a row sees anything of, too)
-            if (kt == it.kt0) {
+            const bool raise = (top - m) * c > kRaise;
+            if (kt == kt0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, raise)) {
-                float f = 1.0f;
-                if (raise) {
-                    f = ex2((m - top) * ca);
+                const float f = raise ? ex2((m - top) * c) : 1.0f;
+                if (raise)
                     m = top;
-                }
                 l *= f;
-#pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    uint32_t o[32];
-                    tmem_ld32(to + x * 32, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                    tmem_st32(to + x * 32, o);
-                }
+                rescale_row<D>(to, f);
             }
-            const float mc = m == -INFINITY ? 0.0f : m * ca;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float mc = m == -INFINITY ? 0.0f : m * c;
+            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int x = 0; x < kDenseTile / 32; ++x) {
                 uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float p0 = ex2(fmaf(s[x * 32 + e], ca, -mc)), p1 = ex2(fmaf(s[x * 32 + e + 1], ca, -mc));
-                    sum[e & 2] += p0;
-                    sum[(e & 2) + 1] += p1;
-                    p[e / 2] = pack_bf16(p0, p1);
+                for (int e = 0; e < 16; ++e) {
+                    float x0, x1;
+                    unpair(fma2(pair(s[x * 32 + 2 * e], s[x * 32 + 2 * e + 1]), c2, mc2), x0, x1);
+                    x0 = ex2(x0);
+                    x1 = ex2(x1);
+                    sum[e & 1] = add2(sum[e & 1], pair(x0, x1));
+                    p[e] = pack_bf16(x0, x1);
                 }
                 tmem_st16(ts + x * 16, p);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float y0, y1;
+            unpair(add2(sum[0], sum[1]), y0, y1);
+            l += y0 + y1;
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.p_ready[stream]);
         }
-        // the item's end: O / l to the output, or O, m and l to the partial results
         if (!warp_wait(&sh.o_full[stream], done & 1, a.ctrl, lane))
             return;
         ++done;
         tmem_fence_after();
-        const bool live = token < tokens, whole = it.slot < 0;
-        const bool bad = sh.bad[k % kItemSlots] != 0;
-        const int64_t row = (it.q_row + stream * T + token) * a.Hq + it.g * a.G + head;
-        float *part = a.part + ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + r) * (D + 4);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
-            tmem_ld32(to + x * 32, o);
-            tmem_wait_ld();
-            if (live && bad) {
-                // infinities and NaN of the masked tiles that this row sees
-                const int64_t t0 = max(masked_from, (int64_t)it.kt0) * kDenseTile;
-                const int64_t t1 = min(pos + 1, (int64_t)it.kt1 * kDenseTile);
-                for (int64_t t = t0; t < t1; ++t) {
-                    const int64_t vr = dense_row(a, it.b, it.off, t);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float y = vr < 0 ? 0.0f : __bfloat162float(a.v[vr * a.st + it.g * a.sh + x * 32 + e]);
-                        if (!isfinite(y))
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-                    }
-                }
-            }
-            if (live && whole) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 w;
-                    w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                    w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                    w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                    w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                    *reinterpret_cast<uint4 *>(a.out + row * D + x * 32 + e) = w;
-                }
-            } else if (live) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4 *>(part + x * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
-            __syncwarp();
-        }
-        if (live) {
-            const float mb = m * fabsf(c);
-            if (!whole)
-                *reinterpret_cast<float2 *>(part + D) = make_float2(mb, l);
-            else if (a.lse != nullptr)
-                a.lse[row] = l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
-        }
+        finish_row<D>(a, sh.ring.item[slot], sh.bad[slot] != 0, stream, r, to, m * c, l);
         tmem_fence_before();
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(&sh.ring.item_empty[k % kItemSlots]);
+            mbar_arrive(&sh.ring.item_empty[slot]);
     }
 }
 
-// ---- the products, issued by one thread -------------------------------------
+// ---- the products -----------------------------------------------------------
+// One lane issues them, but the whole warp walks: what addresses and counts
+// depend on is the same in every lane and stays in uniform registers, where
+// the instruction wants it (a walk of one lane spent 100 cycles an MMA on
+// bringing its operands there, more than the 64 that the product takes).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 template <int D>
-__device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh, uint32_t sq, uint32_t ring)
+__device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh, uint32_t sq, uint32_t ring, int lane)
 {
     constexpr int NS = kStages<D>;
     constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, kDenseTile);
     constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | (1u << 16);   // B's N index is contiguous
     const int T = kStreamRows / a.G;
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
     uint32_t n = 0;                                  // tiles consumed
     uint32_t p_phase[2] = {0, 0}, clean = 0;
-    auto fail = [&]() { report_timeout(a.ctrl, kSiteDense); };
+    // one lane: S of stream s = Q K^T with K in stage st
     auto scores = [&](int s, int st) {
+        const uint64_t q = umma_desc_sw128(sq + s * (kStreamRows * D * 2));
+        const uint64_t k = umma_desc_sw128(ring + st * kTileBytes<D>);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (uint32_t)((ks >> 2) * (128 * 128) + (ks & 3) * 32);
-            umma_bf16(tmem + s * 128, umma_desc_sw128(sq + s * (kStreamRows * D * 2) + off),
-                      umma_desc_sw128(ring + st * kTileBytes<D> + off), idesc_s, ks > 0);
+            const uint64_t off = (uint64_t)(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
+            umma_bf16(tmem + s * 128, q + off, k + off, idesc_s, ks > 0);
         }
         umma_commit(&sh.s_full[s]);
     };
+    // one lane: O of stream s (+)= P V with V in stage st
+    auto values = [&](int s, int st, bool more) {
+        const uint64_t v = umma_desc_sw128_mn(ring + st * kTileBytes<D>, kDenseTile * 128);
+#pragma unroll
+        for (int ks = 0; ks < kDenseTile / 16; ++ks)
+            umma_bf16_ts(tmem + kTmemO + s * D, tmem + s * 128 + ks * 8, v + (uint64_t)(ks * 2048 >> 4), idesc_o,
+                         more || ks > 0);
+    };
     for (uint32_t k = 0;; ++k) {
-        if (!mbar_wait_bounded(&sh.ring.item_full[k % kItemSlots], (k / kItemSlots) & 1, kSpinLimit))
-            return fail();
-        const int32_t b = sh.ring.item[k % kItemSlots].b;
-        if (b < 0)
+        const int slot = k % kItemSlots;
+        if (!warp_wait(&sh.ring.item_full[slot], (k / kItemSlots) & 1, a.ctrl, lane))
             return;
-        const int kt0 = sh.ring.item[k % kItemSlots].kt0, kt1 = sh.ring.item[k % kItemSlots].kt1;
-        const int streams = sh.ring.item[k % kItemSlots].tokens > T ? 2 : 1;
-        const int64_t masked_from = dense_masked_from(sh.ring.item[k % kItemSlots].first_pos);
-        if (!mbar_wait_bounded(&sh.q_full, k & 1, kSpinLimit))
-            return fail();
+        if (uniform(sh.ring.item[slot].b) < 0)
+            return;
+        const int kt0 = uniform(sh.ring.item[slot].kt0), kt1 = uniform(sh.ring.item[slot].kt1);
+        const bool two = uniform(sh.ring.item[slot].tokens) > T;
+        const int masked_from = uniform((int)dense_masked_from(sh.ring.item[slot].first_pos));
+        if (!warp_wait(&sh.q_full, k & 1, a.ctrl, lane))
+            return;
         {
             const int st = n % NS;
-            if (!mbar_wait_bounded(&sh.ring.full[st], (n / NS) & 1, kSpinLimit))
-                return fail();
+            if (!warp_wait(&sh.ring.full[st], (n / NS) & 1, a.ctrl, lane))
+                return;
             tmem_fence_after();
-            for (int s = 0; s < streams; ++s)
-                scores(s, st);
-            umma_commit(&sh.ring.empty[st]);
-            if (kt0 + 1 == kt1)
-                umma_commit(&sh.q_empty);
+            if (elect_one()) {
+                scores(0, st);
+                if (two)
+                    scores(1, st);
+                umma_commit(&sh.ring.empty[st]);
+                if (kt0 + 1 == kt1)
+                    umma_commit(&sh.q_empty);
+            }
+            __syncwarp();
             ++n;
         }
         for (int kt = kt0; kt < kt1; ++kt) {
             const int sv = n % NS, sk = (n + 1) % NS;
             const bool more = kt + 1 < kt1;
-            bool ok;
             if (kt >= masked_from) {
-                ok = mbar_wait_bounded(&sh.clean[sv], (clean >> sv) & 1, kSpinLimit);
+                if (!warp_wait(&sh.clean[sv], (clean >> sv) & 1, a.ctrl, lane))
+                    return;
                 clean ^= 1u << sv;
-            } else {
-                ok = mbar_wait_bounded(&sh.ring.full[sv], (n / NS) & 1, kSpinLimit);
+            } else if (!warp_wait(&sh.ring.full[sv], (n / NS) & 1, a.ctrl, lane)) {
+                return;
             }
-            if (!ok)
-                return fail();
-            for (int s = 0; s < streams; ++s) {
-                if (!mbar_wait_bounded(&sh.p_ready[s], p_phase[s] & 1, kSpinLimit))
-                    return fail();
-                ++p_phase[s];
-                tmem_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < kDenseTile / 16; ++ks)
-                    umma_bf16_ts(tmem + kTmemO + s * D, tmem + s * 128 + ks * 8,
-                                 umma_desc_sw128_mn(ring + sv * kTileBytes<D> + ks * 2048, kDenseTile * 128), idesc_o,
-                                 kt > kt0 || ks > 0);
-                if (s + 1 == streams)
+            if (!warp_wait(&sh.p_ready[0], p_phase[0]++ & 1, a.ctrl, lane))
+                return;
+            tmem_fence_after();
+            if (elect_one()) {
+                values(0, sv, kt > kt0);
+                if (!two)
                     umma_commit(&sh.ring.empty[sv]);
-                if (!more) {
-                    umma_commit(&sh.o_full[s]);
-                    continue;
+                if (!more)
+                    umma_commit(&sh.o_full[0]);
+            }
+            __syncwarp();
+            if (more) {
+                if (!warp_wait(&sh.ring.full[sk], ((n + 1) / NS) & 1, a.ctrl, lane))
+                    return;
+                if (elect_one()) {
+                    scores(0, sk);
+                    if (!two) {
+                        umma_commit(&sh.ring.empty[sk]);
+                        if (kt + 2 == kt1)
+                            umma_commit(&sh.q_empty);
+                    }
                 }
-                if (s == 0 && !mbar_wait_bounded(&sh.ring.full[sk], ((n + 1) / NS) & 1, kSpinLimit))
-                    return fail();
+                __syncwarp();
+            }
+            if (two) {
+                if (!warp_wait(&sh.p_ready[1], p_phase[1]++ & 1, a.ctrl, lane))
+                    return;
                 tmem_fence_after();
-                scores(s, sk);
-                if (s + 1 == streams) {
-                    umma_commit(&sh.ring.empty[sk]);
-                    if (kt + 2 == kt1)
-                        umma_commit(&sh.q_empty);
+                if (elect_one()) {
+                    values(1, sv, kt > kt0);
+                    umma_commit(&sh.ring.empty[sv]);
+                    if (more) {
+                        scores(1, sk);
+                        umma_commit(&sh.ring.empty[sk]);
+                        if (kt + 2 == kt1)
+                            umma_commit(&sh.q_empty);
+                    } else {
+                        umma_commit(&sh.o_full[1]);
+                    }
                 }
+                __syncwarp();
             }
             n += more ? 2 : 1;
         }
-        mbar_arrive(&sh.ring.item_empty[k % kItemSlots]);
+        if (lane == 0)
+            mbar_arrive(&sh.ring.item_empty[slot]);
     }
 }
 
 // ---- V of the masked tiles ---------------------------------------------------
 // A masked token's weight is 0, but 0 times an infinity or NaN is NaN in the
-// product.  So in tiles that some row does not see whole, rows behind the
-// sequence's end become zero, and so do infinite and NaN elements, which the
-// softmax threads add to the rows that do see them.
+// product, and rows behind the sequence's end hold anything.  So tokens that
+// no row of the item sees become zero, and of those that some rows see the
+// infinite and NaN elements, which the softmax threads add to the rows that do.
 template <int D>
 __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, uint8_t *ring, int lane)
 {
@@ -365,7 +454,9 @@ __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, u
         if (sh.ring.item[slot].b < 0)
             return;
         const int kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
-        const int64_t end = sh.ring.item[slot].n, masked_from = dense_masked_from(sh.ring.item[slot].first_pos);
+        // positions of the item's first and last query token
+        const int64_t first = sh.ring.item[slot].first_pos, last = first + sh.ring.item[slot].tokens - 1;
+        const int64_t masked_from = dense_masked_from(first);
         for (int kt = kt0; kt < kt1; ++kt, n += 2) {
             // it waits for and releases every V tile, so that it never falls a
             // turn of the ring behind or ahead of the barriers' phases
@@ -378,18 +469,24 @@ __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, u
                 continue;
             }
             uint4 *tile = reinterpret_cast<uint4 *>(ring + st * kTileBytes<D>);
-            const int64_t left = end - (int64_t)kt * kDenseTile;
+            // tokens seen by all rows, by some, by none (of the tile's 128)
+            const int64_t t0 = (int64_t)kt * kDenseTile;
+            const int all = (int)max(min(first + 1 - t0, (int64_t)kDenseTile), (int64_t)0);
+            const int some = (int)max(min(last + 1 - t0, (int64_t)kDenseTile), (int64_t)all);
             bool bad = false;
-#pragma unroll 8
-            for (int i = lane; i < kTileBytes<D> / 16; i += 32) {
-                const bool own = ((i >> 3) & (kDenseTile - 1)) < left;   // 8 pieces a token's 128-byte row
-                const uint4 x = tile[i];
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (own)
-                    w = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
-                if (w.x != x.x || w.y != x.y || w.z != x.z || w.w != x.w) {
-                    tile[i] = w;
-                    bad |= own;
+            for (int half = 0; half < D / 64; ++half) {
+                uint4 *rows = tile + half * (kDenseTile * 8);   // 8 pieces of 16 bytes a token
+#pragma unroll 4
+                for (int i = some * 8 + lane; i < kDenseTile * 8; i += 32)
+                    rows[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = all * 8 + lane; i < some * 8; i += 32) {
+                    const uint4 x = rows[i];
+                    const uint4 w = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
+                                               finite_or_zero(x.w));
+                    if (w.x != x.x || w.y != x.y || w.z != x.z || w.w != x.w) {
+                        rows[i] = w;
+                        bad = true;
+                    }
                 }
             }
             if (bad)
@@ -417,7 +514,7 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
     uint8_t *sq = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = sq + 2 * kStreamRows * D * 2;
     int64_t *start = reinterpret_cast<int64_t *>(ring + kStages<D> * kTileBytes<D>);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     if (tid == 0) {
         // K tiles have the even stages, read by the MMAs; V tiles the odd
         // ones, read by the MMAs and the guard
@@ -445,23 +542,24 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
     tmem_fence_after();
 
     if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax_stream<D>(a, sh, warp >> 2, warp & 3, lane);
-    } else if (warp == kLoadWarp) {
-        const QueryLoad<D> q = {&qmap, sq, &sh.q_full, &sh.q_empty, sh.bad};
-        load_items<D, kStages<D>, true>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, q);
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            issue_products<D>(a, sh, smem_u32(sq), smem_u32(ring));
-            // every MMA issued has completed before TMEM is released
-            umma_commit(&sh.done);
-            if (!mbar_wait_bounded(&sh.done, 0, kSpinLimit)) {
-                report_timeout(a.ctrl, kSiteDense);
-                (void)mbar_wait_bounded(&sh.done, 0, kSpinLimit);
-            }
-        }
-        __syncwarp();
     } else {
-        guard_values<D>(a, sh, ring, lane);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
+        if (warp == kLoadWarp) {
+            const QueryLoad<D> q = {&qmap, sq, &sh.q_full, &sh.q_empty, sh.bad};
+            load_items<D, kStages<D>, true>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, q);
+        } else if (warp == kMmaWarp) {
+            issue_products<D>(a, sh, smem_u32(sq), smem_u32(ring), lane);
+            // every MMA issued has completed before TMEM is released
+            if (elect_one())
+                umma_commit(&sh.done);
+            __syncwarp();
+            if (!warp_wait(&sh.done, 0, a.ctrl, lane))
+                (void)warp_wait(&sh.done, 0, a.ctrl, lane);
+        } else if (warp == kGuardWarp) {
+            guard_values<D>(a, sh, ring, lane);
+        }
     }
     tmem_fence_before();
     __syncthreads();
