@@ -351,48 +351,66 @@ def ts_quest_select(kv: KVCache, scores, page_size: int, k: int, n_sink: int, n_
 
 # ---- new tokens of many requests: room, cache rows, attention ----
 
-def _on_device(name, t, dtype, device, shape=None):
-    """A contiguous tensor of this type on the current CUDA device (and of
-    this shape): what the kernels below take by address alone."""
+# These calls bring few tokens at a time, so what the binding itself costs
+# counts: each check is one comparison where it holds, and says what is wrong
+# only where it does not.
+
+def _address(name, t, dtype, device: int, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on the
+    current CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("libts computes on the GPU only; %s is a %s tensor" % (name, t.device))
-    if t.device != device:
-        raise ValueError("%s is on %s, the call runs on %s" % (name, t.device, device))
-    if t.dtype != dtype:
+    if t.get_device() != device:
+        _wrong_device(name, t, device)
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have the shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
 
 
-def _token_rows(name, t, heads: int, d: int, device) -> int:
+def _wrong_device(name, t, device: int):
+    if not t.is_cuda:
+        raise ValueError("libts computes on the GPU only; %s is a %s tensor" % (name, t.device))
+    raise ValueError("%s is on %s, the call runs on cuda:%d" % (name, t.device, device))
+
+
+def _token_rows(name, t, heads: int, d: int, device: int) -> int:
     """[tokens, heads, d] bf16 with contiguous heads; returns the token stride
     (a view of a wider projection's output has more than heads * d)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("libts computes on the GPU only; %s is a %s tensor" % (name, t.device))
-    if t.device != device:
-        raise ValueError("%s is on %s, the call runs on %s" % (name, t.device, device))
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != device:
+        _wrong_device(name, t, device)
+    if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be bf16" % name)
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError("%s must be [tokens, %d, %d] (got %s)" % (name, heads, d, tuple(t.shape)))
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError("%s must be [tokens, %d, %d] (got %s)" % (name, heads, d, tuple(shape)))
+    st = t.stride()
+    if shape[0] and (st[2] != 1 or (heads > 1 and st[1] != d)):
         raise ValueError("%s must have contiguous heads of contiguous channels" % name)
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return st[0] if shape[0] > 1 else heads * d
 
 
-def _current_device():
-    return torch.device("cuda", torch.cuda.current_device())
+def _cache_on(kv: KVCache, device: int):
+    if kv.k.get_device() != device:
+        _wrong_device("the cache", kv.k, device)
 
 
-def _cache_on(kv: KVCache, device):
-    if kv.k.device != device:
-        raise ValueError("the cache is on %s, the call runs on %s" % (kv.k.device, device))
+def _raw_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _host_offsets(offsets, batch: int) -> np.ndarray:
+    off = offsets
+    if type(off) is not np.ndarray or off.dtype != np.int64 or not off.flags.c_contiguous:
+        off = np.ascontiguousarray(np.asarray(offsets, dtype=np.int64))
+    if off.shape != (batch + 1,):
+        raise ValueError("offsets must have %d entries (got %s)" % (batch + 1, off.shape))
+    return off
 
 
 def ts_extend_pages(cached, fresh, page_size: int, free_pages, pool_pages: int, page_table, seq_offsets, q_offsets,
@@ -403,34 +421,30 @@ def ts_extend_pages(cached, fresh, page_size: int, free_pages, pool_pages: int, 
     slots int64 [at least the new tokens] and pages_used int64 [1] written."""
     if not isinstance(cached, torch.Tensor) or not cached.is_cuda:
         raise ValueError("libts computes on the GPU only; cached must be a CUDA tensor")
-    dev, B = _current_device(), cached.shape[0] if cached.dim() == 1 else -1
-    for name, t in (("cached", cached), ("fresh", fresh)):
-        _on_device(name, t, torch.int64, dev, (B,))
-    for name, t in (("seq_offsets", seq_offsets), ("q_offsets", q_offsets)):
-        _on_device(name, t, torch.int64, dev, (B + 1,))
-    _on_device("free_pages", free_pages, torch.int32, dev, (free_pages.numel(),))
-    _on_device("slots", slots, torch.int64, dev, (slots.numel(),))
-    _on_device("pages_used", pages_used, torch.int64, dev, (1,))
-    _on_device("page_table", page_table, torch.int32, dev)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [batch, stride]")
-    _check(_lib.ts_extend_pages(B, _ptr(cached), _ptr(fresh), int(page_size), _ptr(free_pages), free_pages.numel(),
-                                int(pool_pages), _ptr(page_table), page_table.shape[1], _ptr(seq_offsets),
-                                _ptr(q_offsets), _ptr(slots), slots.numel(), _ptr(pages_used), _stream(stream)))
+    if cached.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != cached.shape[0]:
+        raise ValueError("cached must be [batch] and page_table [batch, stride]")
+    dev, B, i64 = torch.cuda.current_device(), cached.shape[0], torch.int64
+    n_free, n_slots, stride = free_pages.numel(), slots.numel(), page_table.shape[1]
+    _check(_lib.ts_extend_pages(
+        B, _address("cached", cached, i64, dev, (B,)), _address("fresh", fresh, i64, dev, (B,)), page_size,
+        _address("free_pages", free_pages, torch.int32, dev, (n_free,)), n_free, pool_pages,
+        _address("page_table", page_table, torch.int32, dev, (B, stride)), stride,
+        _address("seq_offsets", seq_offsets, i64, dev, (B + 1,)), _address("q_offsets", q_offsets, i64, dev, (B + 1,)),
+        _address("slots", slots, i64, dev, (n_slots,)), n_slots, _address("pages_used", pages_used, i64, dev, (1,)),
+        _raw_stream(stream, dev)))
 
 
 def ts_write_kv(kv: KVCache, k_new, v_new, slots, stream=None):
     """K and V rows of new tokens ([n, h_kv, d] bf16; views of a projection's
     output, of equal token stride) to the token rows slots (int64 [n]) of the
     cache; rows with a slot outside the cache go nowhere."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     _cache_on(kv, dev)
-    st = _token_rows("k_new", k_new, kv.h_kv, kv.head_dim, dev)
-    if v_new.shape != k_new.shape or _token_rows("v_new", v_new, kv.h_kv, kv.head_dim, dev) != st:
+    n, st = k_new.shape[0], _token_rows("k_new", k_new, kv.h_kv, kv.head_dim, dev)
+    if _token_rows("v_new", v_new, kv.h_kv, kv.head_dim, dev) != st or v_new.shape[0] != n:
         raise ValueError("k_new and v_new must have the same shape and token stride")
-    _on_device("slots", slots, torch.int64, dev, (k_new.shape[0],))
-    _check(_lib.ts_write_kv(kv.ref(), _ptr(kv.k), _ptr(kv.v), _ptr(k_new), _ptr(v_new), st, _ptr(slots),
-                            k_new.shape[0], _stream(stream)))
+    _check(_lib.ts_write_kv(kv.ref(), kv.struct.k, kv.struct.v, k_new.data_ptr(), v_new.data_ptr(), st,
+                            _address("slots", slots, torch.int64, dev, (n,)), n, _raw_stream(stream, dev)))
 
 
 def ts_dense_attn_workspace_bytes(kv: KVCache, q_offsets_host) -> int:
@@ -445,28 +459,24 @@ def ts_dense_attn(kv: KVCache, q, q_offsets_dev, q_offsets_host, out, lse, ws, s
     """Causal attention of each sequence's newest tokens (q [n, h_q, d] bf16,
     rows q_offsets[b] .. q_offsets[b+1] of sequence b) over all of its cached
     tokens; out bf16 [n, h_q, d], lse float32 [n, h_q] or None."""
-    dev = _current_device()
+    dev = torch.cuda.current_device()
     _cache_on(kv, dev)
     off = _host_offsets(q_offsets_host, kv.batch)
-    rows = int(off[-1])
-    st = _token_rows("q", q, kv.h_q, kv.head_dim, dev)
-    _on_device("q_offsets_dev", q_offsets_dev, torch.int64, dev, (kv.batch + 1,))
-    _on_device("out", out, torch.bfloat16, dev)
-    if q.shape[0] < rows or out.dim() != 3 or out.shape[0] < rows or out.shape[1:] != q.shape[1:]:
+    rows, h_q, d = int(off[-1]), kv.h_q, kv.head_dim
+    st = _token_rows("q", q, h_q, d, dev)
+    n_out = out.shape[0]
+    if q.shape[0] < rows or n_out < rows:
         raise ValueError("q and out must hold the %d query rows" % rows)
     if lse is not None:
-        _on_device("lse", lse, torch.float32, dev)
-        if lse.dim() != 2 or lse.shape[0] < rows or lse.shape[1] != kv.h_q:
-            raise ValueError("lse must be [rows, h_q]")
-    _check(_lib.ts_dense_attn(kv.ref(), _ptr(q), st, _ptr(q_offsets_dev), off.ctypes.data, _ptr(out), _ptr(lse),
-                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
-
-
-def _host_offsets(offsets, batch: int) -> np.ndarray:
-    off = np.ascontiguousarray(np.asarray(offsets, dtype=np.int64))
-    if off.shape != (batch + 1,):
-        raise ValueError("offsets must have %d entries (got %s)" % (batch + 1, off.shape))
-    return off
+        if lse.shape[0] < rows:
+            raise ValueError("lse must hold the %d query rows" % rows)
+        lse = _address("lse", lse, torch.float32, dev, (lse.shape[0], h_q))
+    if ws.get_device() != dev:
+        _wrong_device("ws", ws, dev)
+    _check(_lib.ts_dense_attn(
+        kv.ref(), q.data_ptr(), st, _address("q_offsets_dev", q_offsets_dev, torch.int64, dev, (kv.batch + 1,)),
+        off.__array_interface__["data"][0], _address("out", out, torch.bfloat16, dev, (n_out, h_q, d)), lse,
+        ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev)))
 
 
 def ts_status_string(status: int) -> str:

@@ -96,7 +96,6 @@ dense_merge(const DenseArgs a, int blocks, int slot_rows)
 
 }  // namespace
 
-size_t dense_tc_smem(int D, int B);
 cudaError_t launch_dense_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                             const DenseArgs &a, int D, int box, int grid, cudaStream_t st);
 cudaError_t launch_dense_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int D, int box,

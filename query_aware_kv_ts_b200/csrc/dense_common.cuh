@@ -78,8 +78,9 @@ __device__ __forceinline__ int64_t items_cost(const DenseArgs &a, int64_t base, 
     return t * (base + kItemCost) + (int64_t)a.TT * (t * (t + 1) / 2);
 }
 
-// The line's sequence boundaries in start[0..B] (shared memory).  Every
-// thread of the block calls it.
+// The line's sequence boundaries in start[0..B] (shared memory; only begin()
+// below reads them, before the block's first load, so they may lie where the
+// tiles will).  Every thread of the block calls it.
 __device__ __forceinline__ void dense_line(const DenseArgs &a, int64_t *start, int64_t *s_warp)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,6 +119,20 @@ __device__ __forceinline__ void dense_line(const DenseArgs &a, int64_t *start, i
     __syncthreads();
 }
 
+// The first sequence from b on that has items, B if none has.  Whole warp, 32
+// sequences a round trip.
+__device__ __forceinline__ int dense_next_seq(const DenseArgs &a, int b)
+{
+    for (; b < a.B; b += 32) {
+        const int i = b + (threadIdx.x & 31);
+        const bool has = i < a.B && seq_items(a, __ldcg(a.q_off + i + 1) - __ldcg(a.q_off + i)) > 0;
+        const uint32_t vote = __ballot_sync(0xffffffffu, has);
+        if (vote)
+            return b + __ffs(vote) - 1;
+    }
+    return a.B;
+}
+
 // A place on the line, at a tile boundary of an item (b == B: its end).
 struct DensePlace {
     int32_t b, g, t, cut;
@@ -137,16 +152,14 @@ __device__ __forceinline__ void dense_load_seq(const DenseArgs &a, DensePlace &p
     p.f = __ldcg(a.q_off + p.b + 1) - __ldcg(a.q_off + p.b);
 }
 
-__device__ __forceinline__ void dense_next_item(const DenseArgs &a, const int64_t *start, DensePlace &p)
+__device__ __forceinline__ void dense_next_item(const DenseArgs &a, DensePlace &p)
 {
     p.cut = 0;
     if (++p.t >= seq_items(a, p.f)) {
         p.t = 0;
         if (++p.g == a.Hkv) {
             p.g = 0;
-            do {
-                ++p.b;
-            } while (p.b < a.B && start[p.b + 1] == start[p.b]);
+            p.b = dense_next_seq(a, p.b + 1);
             if (p.b < a.B)
                 dense_load_seq(a, p);
         }
@@ -202,12 +215,12 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int
         p.cut = 2 * rem < base + (t0 + 1) * a.TT + kItemCost ? 0 : p.tiles;
     }
     if (p.cut == p.tiles)
-        dense_next_item(a, start, p);
+        dense_next_item(a, p);
     return p;
 }
 
 // The pieces of block c, one after another: next() is false at the end of
-// its part.  One thread walks (or all of a warp alike).
+// its part.  All lanes of a warp walk alike.
 struct DenseWalk {
     DensePlace at, end;
 
@@ -231,7 +244,7 @@ struct DenseWalk {
             p.flags = kPieceThrough | kPieceEmpty;
         return p;
     }
-    __device__ __forceinline__ bool next(const DenseArgs &a, const int64_t *start, DenseItem &it)
+    __device__ __forceinline__ bool next(const DenseArgs &a, DenseItem &it)
     {
         if (at.b >= a.B)
             return false;
@@ -253,7 +266,7 @@ struct DenseWalk {
         if (last)
             at.cut = end.cut;                                // next() ends here
         else
-            dense_next_item(a, start, at);
+            dense_next_item(a, at);
         return true;
     }
 };
@@ -306,12 +319,11 @@ struct DenseRing {
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     DenseItem item[kItemSlots];
 
-    // arrivals that free an even stage, an odd one, an item
-    __device__ void init(int stages, int even_readers, int odd_readers, int item_readers)
+    __device__ void init(int stages, int tile_readers, int item_readers)
     {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], s & 1 ? odd_readers : even_readers);
+            mbar_init(&empty[s], tile_readers);
         }
         for (int s = 0; s < kItemSlots; ++s) {
             mbar_init(&item_full[s], 1);
@@ -345,13 +357,30 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Whole warp: wait for a barrier's phase, bounded; false when it gave up.
+// Whole warp: wait for a barrier's phase, bounded (each try suspends the warp
+// for a while); false when it gave up.  The loop is one asm block: a wait on a
+// phase that is there already costs one try and one branch, on which the
+// tensor cores wait between products.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *ctrl, int lane)
 {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kSpinLimit));
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "WAIT_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT_%=;\n\t"
+        "DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSpinLimit)
+        : "memory");
     if (!ok && lane == 0)
         report_timeout(ctrl, kSiteDense);
-    return ok;
+    return ok != 0;
 }
 
 // The loading warp: walks the block's items, publishes each, and streams its
@@ -372,6 +401,8 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     const int64_t oob = a.pool_pages << a.page_shift;   // past the pool: reads zeros
     DenseWalk w;
     w.begin(a, start);
+    __syncwarp();
+    fence_proxy_async_smem();                        // start's reads are done: tiles may go over it
     if (lane == 0)
         a.pieces[blockIdx.x] = w.piece(a);
     uint32_t n = 0;                                  // tiles loaded (K and V count one each)
@@ -379,7 +410,7 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     bool ok = true;
     uint32_t k = 0;
     for (; ok; ++k) {
-        const bool more = w.next(a, start, it);
+        const bool more = w.next(a, it);
         const int slot = k % kItemSlots;
         if (k >= kItemSlots && !warp_wait(&r.item_empty[slot], ((k / kItemSlots) - 1) & 1, a.ctrl, lane)) {
             ok = false;

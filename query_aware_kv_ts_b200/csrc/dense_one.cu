@@ -277,10 +277,10 @@ dense_one(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     __shared__ OneShared sh;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     float *join = reinterpret_cast<float *>(ring + kOneStages<D, WIDE> * kTileBytes<D>);
-    int64_t *start = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(join) + kJoinBytes<D, WIDE>);
+    int64_t *start = reinterpret_cast<int64_t *>(ring);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        sh.ring.init(kOneStages<D, WIDE>, kOneWarps, kOneWarps, kOneWarps);
+        sh.ring.init(kOneStages<D, WIDE>, kOneWarps, kOneWarps);
         mbar_init(&sh.joined, kOneWarps);
         mbar_init(&sh.join_free, kOneWarps);
         mbar_fence_init();
@@ -302,7 +302,7 @@ template <int D, bool WIDE>
 cudaError_t launch_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int box, int grid,
                        cudaStream_t st)
 {
-    const size_t smem = 1024 + (size_t)kOneStages<D, WIDE> * kTileBytes<D> + kJoinBytes<D, WIDE> + (a.B + 1) * 8;
+    const size_t smem = 1024 + (size_t)kOneStages<D, WIDE> * kTileBytes<D> + kJoinBytes<D, WIDE>;
     const cudaError_t e = ensure_dyn_smem((const void *)dense_one<D, WIDE>, (int)smem);
     if (e != cudaSuccess)
         return e;

@@ -14,10 +14,6 @@
 // ring of tiles; warp 9 issues the MMAs; warp 10 clears what a masked token
 // must not leak out of V.  While one stream's softmax runs, the tensor cores
 // do the other's products.
-//
-// The maximum is only raised when a row's new one is 2^8 above the old (the
-// weights then stay below 2^8, far from fp32's limits, and the result is
-// divided by a sum with the same reference), so O is rarely rescaled.
 #include "dense_common.cuh"
 
 namespace ts {
@@ -27,22 +23,20 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;   // and an idle one
 constexpr int kTcThreads = 12 * 32;
 // Registers: 384 threads x 168 at launch; the loading, issuing and guarding
-// warps' group gives up some, the two softmax groups take them
+// warps' group gives some to the two softmax groups
 // (128 x 96 + 256 x 200 <= 384 x 168).
 constexpr int kAuxRegs = 96, kSoftmaxRegs = 200;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;            // S (and P over it) at 0 and 128, O at 256 and 256 + d
-constexpr float kRaise = 8.0f;              // log2 of how far weights may grow before O is rescaled
+constexpr float kRaise = 4096.0f;           // sum of a tile's weights above which the reference is raised
 
-constexpr int kTcRingBytes = 128 * 1024;    // K / V tiles
-template <int D>
-constexpr int kStages = kTcRingBytes / kTileBytes<D>;   // even: K and V take turns
+constexpr int kTcMaxStages = 8;
 
 struct TcShared {
-    DenseRing<8> ring;
+    DenseRing<kTcMaxStages> ring;
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_ready[2], o_full[2];
-    uint64_t clean[8];                       // the masked V tile in this stage has been cleared
+    uint64_t clean[kTcMaxStages];                       // the masked V tile in this stage has been cleared
     uint64_t done;
     int32_t bad[kItemSlots];                 // the item's masked tiles held infinities or NaN in V
     uint32_t tmem;
@@ -127,40 +121,76 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// O of this row times f.
-template <int D>
-__device__ __forceinline__ void rescale_row(uint32_t to, float f)
+// 32 weights 2^(s c - mc): their sum added to sum, as bf16 in p.  (A share of
+// them by a polynomial on the FMA units, beside the exponential unit, was
+// 2-5 % slower in long runs: those run at the power limit, where what counts
+// is the number of operations.)
+__device__ __forceinline__ void weights32(const float *s, uint64_t c2, uint64_t mc2, uint64_t *sum, uint32_t *p)
 {
-#pragma unroll 1
-    for (int x = 0; x < D / 16; ++x) {
-        uint32_t o[16];
-        tmem_ld_32x32b<16>(to + x * 16, o);
-        tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-        tmem_st16(to + x * 16, o);
+    for (int e = 0; e < 16; ++e) {
+        float y0, y1;
+        unpair(fma2(pair(s[2 * e], s[2 * e + 1]), c2, mc2), y0, y1);
+        y0 = ex2(y0);
+        y1 = ex2(y1);
+        sum[e & 1] = add2(sum[e & 1], pair(y0, y1));
+        p[e] = pack_bf16(y0, y1);
     }
 }
 
-// The item's end for this thread's row: O / l to the output, or O, m and l to
-// the partial results.  mb: the row's reference in base 2.
+// 4 x 4 pieces of 16 bytes across 4 lanes: lane i's piece j becomes lane j's
+// piece i.
+__device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane)
+{
+    auto swap = [&](uint4 &x, uint4 &y, int bit) {      // lanes with the bit give x and get y, the others the reverse
+        const bool up = lane & bit;
+        uint4 g = up ? x : y;
+        g.x = __shfl_xor_sync(0xffffffffu, g.x, bit);
+        g.y = __shfl_xor_sync(0xffffffffu, g.y, bit);
+        g.z = __shfl_xor_sync(0xffffffffu, g.z, bit);
+        g.w = __shfl_xor_sync(0xffffffffu, g.w, bit);
+        if (up)
+            x = g;
+        else
+            y = g;
+    };
+    swap(w[0], w[1], 1);
+    swap(w[2], w[3], 1);
+    swap(w[0], w[2], 2);
+    swap(w[1], w[3], 2);
+}
+
+// The item's end for this thread's row: O / l to the output, or O, m and
+// l to the partial results.  mb: the row's reference in base 2.  Four lanes
+// exchange 16-byte pieces first, so that a store covers 8 rows of 64 bytes
+// and not 32 of 16.
 template <int D>
 __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &it, bool bad, int stream, int r,
-                                           uint32_t to, float mb, float l)
+                                           int lane, uint32_t to, float mb, float l)
 {
     const int T = kStreamRows / a.G;
-    const int token = r / a.G, head = r - token * a.G;
-    const bool live = token < min(T, it.tokens - stream * T), whole = it.slot < 0;
-    const int64_t row = (it.q_row + stream * T + token) * a.Hq + it.g * a.G + head;
-    float *part = a.part + ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + r) * (D + 4);
+    const int tokens = min(T, it.tokens - stream * T);
+    const bool whole = it.slot < 0;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int quad = r & ~3, piece = lane & 3;
+    // the rows of this lane's quad: where they go in the output, and (in out-
+    // and part-row order) whether they are rows of the item
+    int64_t base[4];
+    bool live[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int token = (quad + u) / a.G, head = (quad + u) - token * a.G;
+        live[u] = token < tokens;
+        base[u] = whole ? ((it.q_row + stream * T + token) * a.Hq + it.g * a.G + head) * D
+                        : ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + quad + u) * (D + 4);
+    }
 #pragma unroll 1
-    for (int x = 0; x < D / 32; ++x) {
+    for (int x = 0; x < D; x += 32) {
         uint32_t o[32];
-        tmem_ld32(to + x * 32, o);
+        tmem_ld32(to + x, o);
         tmem_wait_ld();
-        if (live && bad) {
+        const int token = r / a.G;
+        if (bad && token < tokens) {
             // infinities and NaN of the masked tiles that this row sees
             const int64_t pos = it.first_pos + stream * T + token;
             const int64_t t0 = max(it.first_pos + 1, (int64_t)it.kt0 * kDenseTile);
@@ -169,38 +199,116 @@ __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &
                 const int64_t vr = dense_row(a, it.b, it.off, t);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const float y = vr < 0 ? 0.0f : __bfloat162float(a.v[vr * a.st + it.g * a.sh + x * 32 + e]);
+                    const float y = vr < 0 ? 0.0f : __bfloat162float(a.v[vr * a.st + it.g * a.sh + x + e]);
                     if (!isfinite(y))
                         o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
                 }
             }
         }
-        if (live && whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-                uint4 w;
-                w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                *reinterpret_cast<uint4 *>(a.out + row * D + x * 32 + e) = w;
-            }
-        } else if (live) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4 *>(part + x * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
         __syncwarp();
+        uint4 w[4];
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t *y = o + 8 * j;
+                w[j].x = pack_bf16(__uint_as_float(y[0]) * inv, __uint_as_float(y[1]) * inv);
+                w[j].y = pack_bf16(__uint_as_float(y[2]) * inv, __uint_as_float(y[3]) * inv);
+                w[j].z = pack_bf16(__uint_as_float(y[4]) * inv, __uint_as_float(y[5]) * inv);
+                w[j].w = pack_bf16(__uint_as_float(y[6]) * inv, __uint_as_float(y[7]) * inv);
+            }
+            transpose4(w, lane);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (live[u])
+                    *reinterpret_cast<uint4 *>(a.out + base[u] + x + piece * 8) = w[u];
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = make_uint4(o[16 * h + 4 * j], o[16 * h + 4 * j + 1], o[16 * h + 4 * j + 2],
+                                      o[16 * h + 4 * j + 3]);
+                transpose4(w, lane);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (live[u])
+                        *reinterpret_cast<uint4 *>(a.part + base[u] + x + h * 16 + piece * 4) = w[u];
+            }
+        }
     }
-    if (live) {
-        if (!whole)
-            *reinterpret_cast<float2 *>(part + D) = make_float2(mb, l);
-        else if (a.lse != nullptr)
-            a.lse[row] = l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
+    const int token = r / a.G, head = r - token * a.G;
+    if (token < tokens && !whole)
+        *reinterpret_cast<float2 *>(a.part + ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + r) *
+                                                 (D + 4) + D) = make_float2(mb, l);
+    else if (token < tokens && a.lse != nullptr)
+        a.lse[(it.q_row + stream * T + token) * a.Hq + it.g * a.G + head] =
+            l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
+}
+
+__device__ __forceinline__ void load_scores(uint32_t ts, bool negative, float (&s)[32])
+{
+    uint32_t *y = reinterpret_cast<uint32_t *>(s);
+    tmem_ld32(ts, y);
+    tmem_wait_ld();
+    // (nothing that uses them moves above the wait)
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+        asm volatile("" : "+r"(y[e]), "+r"(y[e + 1]), "+r"(y[e + 2]), "+r"(y[e + 3]), "+r"(y[e + 4]), "+r"(y[e + 5]),
+                          "+r"(y[e + 6]), "+r"(y[e + 7]));
+    if (negative) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            s[e] = -s[e];
     }
 }
 
-// ---- the softmax of one stream: 128 threads, one row each ------------------
+// One tile's weights 2^((S - m) c) of this thread's row: as bf16 in p, and
+// their sum.  limit: the tokens that the row sees.
+template <bool MASKED>
+__device__ __forceinline__ float tile_weights(uint32_t ts, float m, float c, bool negative, int limit, uint32_t *p)
+{
+    const float mc = m == -INFINITY ? 0.0f : m * c;
+    const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int x = 0; x < kDenseTile / 32; ++x) {
+        float s[32];
+        load_scores(ts + x * 32, negative, s);
+        if (MASKED) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                s[e] = x * 32 + e < limit ? s[e] : -INFINITY;
+        }
+        weights32(s, c2, mc2, sum, p + x * 16);
+    }
+    float y0, y1;
+    unpair(add2(sum[0], sum[1]), y0, y1);
+    return y0 + y1;
+}
+
+// The largest score that the row sees in the tile.
+__device__ __forceinline__ float tile_top(uint32_t ts, bool negative, int limit)
+{
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int x = 0; x < kDenseTile / 32; ++x) {
+        float s[32];
+        load_scores(ts + x * 32, negative, s);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            top[e & 1] = fmaxf(top[e & 1], x * 32 + e < limit ? s[e] : -INFINITY);
+    }
+    return fmaxf(top[0], top[1]);
+}
+
+// ---- the softmax of one stream: 128 threads, one row each -------------------
+// A row's reference m is the maximum of its first tile.  A later tile's
+// weights are taken with m as it stands: they may grow above 1, and their sum
+// tells when they do.  Only when a row's sum passes kRaise is its maximum
+// found, m raised, O rescaled and the tile done again: fp32 and bf16 keep
+// their relative precision at any m, and the result is divided by a sum with
+// the same reference.  (The maximum of every tile, first, would be 300 cycles
+// more between S and P, which the tensor cores wait for.)
 template <int D>
 __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh, int stream, int quarter, int lane)
 {
@@ -224,7 +332,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
         }
         const int kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
         const int masked_from = (int)dense_masked_from(sh.ring.item[slot].first_pos);
-        // tokens that this row sees from tile kt0 on
+        // tokens that the row sees from tile kt0 on
         int64_t left = sh.ring.item[slot].first_pos + first + r / a.G + 1 - (int64_t)kt0 * kDenseTile;
         float m = -INFINITY, l = 0.0f;               // m in units of S
         for (int kt = kt0; kt < kt1; ++kt, left -= kDenseTile) {
@@ -232,62 +340,42 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
                 return;
             ++phase;
             tmem_fence_after();
-            float s[kDenseTile];
+            const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
+            bool raise = kt == kt0 || m == -INFINITY;   // no reference yet
+            uint32_t p[kDenseTile / 2];
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int again = 0; again < 2; ++again) {
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float top = tile_top(ts, negative, limit);
+                    float f = 1.0f;
+                    if (raise && top > m) {
+                        f = ex2((m - top) * c);
+                        m = top;
+                    }
+                    l *= f;
+                    if (kt > kt0) {                  // O of this row times f
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b<16>(to + x, o);
+                            tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < kDenseTile / 32; ++x)
-                tmem_ld32(ts + x * 32, reinterpret_cast<uint32_t *>(s) + x * 32);
-            tmem_wait_ld();
-            if (negative) {
-#pragma unroll
-                for (int x = 0; x < kDenseTile; ++x)
-                    s[x] = -s[x];
-            }
-            if (kt >= masked_from) {
-                const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
-#pragma unroll
-                for (int x = 0; x < kDenseTile; ++x)
-                    s[x] = x < limit ? s[x] : -INFINITY;
-            }
-            float mx[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                mx[u] = fmaxf(s[u], s[u + 4]);
-#pragma unroll
-            for (int x = 8; x < kDenseTile; x += 8)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    mx[u] = fmaxf(mx[u], fmaxf(s[x + u], s[x + u + 4]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool raise = (top - m) * c > kRaise;
-            if (kt == kt0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? ex2((m - top) * c) : 1.0f;
-                if (raise)
-                    m = top;
-                l *= f;
-                rescale_row<D>(to, f);
-            }
-            const float mc = m == -INFINITY ? 0.0f : m * c;
-            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int x = 0; x < kDenseTile / 32; ++x) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float x0, x1;
-                    unpair(fma2(pair(s[x * 32 + 2 * e], s[x * 32 + 2 * e + 1]), c2, mc2), x0, x1);
-                    x0 = ex2(x0);
-                    x1 = ex2(x1);
-                    sum[e & 1] = add2(sum[e & 1], pair(x0, x1));
-                    p[e] = pack_bf16(x0, x1);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(to + x, o);
+                        }
+                    }
                 }
-                tmem_st16(ts + x * 16, p);
+                sum = kt >= masked_from ? tile_weights<true>(ts, m, c, negative, limit, p)
+                                        : tile_weights<false>(ts, m, c, negative, limit, p);
+                raise = sum > kRaise;
+                if (kt == kt0 || !__any_sync(0xffffffffu, raise))
+                    break;
             }
-            float y0, y1;
-            unpair(add2(sum[0], sum[1]), y0, y1);
-            l += y0 + y1;
+            l += sum;
+            tmem_st32(ts, p);
+            tmem_st32(ts + 32, p + 32);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
@@ -298,7 +386,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
             return;
         ++done;
         tmem_fence_after();
-        finish_row<D>(a, sh.ring.item[slot], sh.bad[slot] != 0, stream, r, to, m * c, l);
+        finish_row<D>(a, sh.ring.item[slot], sh.bad[slot] != 0, stream, r, lane, to, m * c, l);
         tmem_fence_before();
         __syncwarp();
         if (lane == 0)
@@ -322,10 +410,9 @@ __device__ __forceinline__ bool elect_one()
 
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-template <int D>
+template <int D, int NS>
 __device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh, uint32_t sq, uint32_t ring, int lane)
 {
-    constexpr int NS = kStages<D>;
     constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, kDenseTile);
     constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | (1u << 16);   // B's N index is contiguous
     const int T = kStreamRows / a.G;
@@ -388,6 +475,10 @@ __device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh,
             } else if (!warp_wait(&sh.ring.full[sv], (n / NS) & 1, a.ctrl, lane)) {
                 return;
             }
+            // (the next K before P: it is there long before, and a wait between
+            // two products would leave the tensor cores idle)
+            if (more && !warp_wait(&sh.ring.full[sk], ((n + 1) / NS) & 1, a.ctrl, lane))
+                return;
             if (!warp_wait(&sh.p_ready[0], p_phase[0]++ & 1, a.ctrl, lane))
                 return;
             tmem_fence_after();
@@ -395,23 +486,18 @@ __device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh,
                 values(0, sv, kt > kt0);
                 if (!two)
                     umma_commit(&sh.ring.empty[sv]);
-                if (!more)
-                    umma_commit(&sh.o_full[0]);
-            }
-            __syncwarp();
-            if (more) {
-                if (!warp_wait(&sh.ring.full[sk], ((n + 1) / NS) & 1, a.ctrl, lane))
-                    return;
-                if (elect_one()) {
+                if (more) {
                     scores(0, sk);
                     if (!two) {
                         umma_commit(&sh.ring.empty[sk]);
                         if (kt + 2 == kt1)
                             umma_commit(&sh.q_empty);
                     }
+                } else {
+                    umma_commit(&sh.o_full[0]);
                 }
-                __syncwarp();
             }
+            __syncwarp();
             if (two) {
                 if (!warp_wait(&sh.p_ready[1], p_phase[1]++ & 1, a.ctrl, lane))
                     return;
@@ -442,10 +528,9 @@ __device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh,
 // product, and rows behind the sequence's end hold anything.  So tokens that
 // no row of the item sees become zero, and of those that some rows see the
 // infinite and NaN elements, which the softmax threads add to the rows that do.
-template <int D>
+template <int D, int NS>
 __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, uint8_t *ring, int lane)
 {
-    constexpr int NS = kStages<D>;
     uint32_t n = 0;
     for (uint32_t k = 0;; ++k) {
         const int slot = k % kItemSlots;
@@ -458,8 +543,12 @@ __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, u
         const int64_t first = sh.ring.item[slot].first_pos, last = first + sh.ring.item[slot].tokens - 1;
         const int64_t masked_from = dense_masked_from(first);
         for (int kt = kt0; kt < kt1; ++kt, n += 2) {
-            // it waits for and releases every V tile, so that it never falls a
-            // turn of the ring behind or ahead of the barriers' phases
+            // it waits for and releases every tile, K's too, so that it never
+            // falls a turn of the ring behind or ahead of the barriers' phases
+            if (!warp_wait(&sh.ring.full[n % NS], (n / NS) & 1, a.ctrl, lane))
+                return;
+            if (lane == 0)
+                mbar_arrive(&sh.ring.empty[n % NS]);
             const int st = (n + 1) % NS;
             if (!warp_wait(&sh.ring.full[st], ((n + 1) / NS) & 1, a.ctrl, lane))
                 return;
@@ -504,22 +593,25 @@ __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, u
     }
 }
 
-template <int D>
+template <int D, int NS>
 __global__ void __launch_bounds__(kTcThreads, 1)
 dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DenseArgs a, int box)
 {
-    extern __shared__ uint8_t dyn_smem[];
-    __shared__ TcShared sh;
-    uint8_t *sq = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
-    uint8_t *ring = sq + 2 * kStreamRows * D * 2;
-    int64_t *start = reinterpret_cast<int64_t *>(ring + kStages<D> * kTileBytes<D>);
+    // all of it dynamic, without padding: five 32 KB tiles and Q leave 3 KB
+    extern __shared__ __align__(1024) uint8_t dyn_smem[];
+    uint8_t *sq = dyn_smem, *ring = sq + 2 * kStreamRows * D * 2;
+    TcShared &sh = *reinterpret_cast<TcShared *>(ring + NS * kTileBytes<D>);
+    int64_t *start = reinterpret_cast<int64_t *>(ring);
+    if (smem_u32(dyn_smem) & 1023u) {                // (the swizzle's atoms are 1024 bytes)
+        if (threadIdx.x == 0)
+            report_timeout(a.ctrl, kSiteDense);
+        return;
+    }
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     if (tid == 0) {
-        // K tiles have the even stages, read by the MMAs; V tiles the odd
-        // ones, read by the MMAs and the guard
-        sh.ring.init(kStages<D>, 1, 2, kSoftmaxWarps + 2);
-        for (int s = 0; s < kStages<D>; ++s)
+        sh.ring.init(NS, 2, kSoftmaxWarps + 2);      // a tile is freed by the MMAs and the guard
+        for (int s = 0; s < NS; ++s)
             mbar_init(&sh.clean[s], 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
@@ -548,9 +640,9 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
         if (warp == kLoadWarp) {
             const QueryLoad<D> q = {&qmap, sq, &sh.q_full, &sh.q_empty, sh.bad};
-            load_items<D, kStages<D>, true>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, q);
+            load_items<D, NS, true>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, q);
         } else if (warp == kMmaWarp) {
-            issue_products<D>(a, sh, smem_u32(sq), smem_u32(ring), lane);
+            issue_products<D, NS>(a, sh, smem_u32(sq), smem_u32(ring), lane);
             // every MMA issued has completed before TMEM is released
             if (elect_one())
                 umma_commit(&sh.done);
@@ -558,7 +650,7 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
             if (!warp_wait(&sh.done, 0, a.ctrl, lane))
                 (void)warp_wait(&sh.done, 0, a.ctrl, lane);
         } else if (warp == kGuardWarp) {
-            guard_values<D>(a, sh, ring, lane);
+            guard_values<D, NS>(a, sh, ring, lane);
         }
     }
     tmem_fence_before();
@@ -570,21 +662,23 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
 
 }  // namespace
 
-size_t dense_tc_smem(int D, int B)
+template <int D, int NS>
+static cudaError_t launch_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                             const DenseArgs &a, int box, int grid, cudaStream_t st)
 {
-    return 1024 + (size_t)2 * kStreamRows * D * 2 + kTcRingBytes + (size_t)(B + 1) * 8;
+    constexpr size_t smem = (size_t)2 * kStreamRows * D * 2 + (size_t)NS * kTileBytes<D> + sizeof(TcShared);
+    static_assert(smem <= 227 * 1024 && (kMaxBatch + 1) * 8 <= NS * kTileBytes<D>, "shared memory");
+    const cudaError_t e = ensure_dyn_smem((const void *)dense_tc<D, NS>, (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    return launch_ex(dense_tc<D, NS>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a, box);
 }
 
 cudaError_t launch_dense_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                             const DenseArgs &a, int D, int box, int grid, cudaStream_t st)
 {
-    const size_t smem = dense_tc_smem(D, a.B);
-    const void *kernel = D == 128 ? (const void *)dense_tc<128> : (const void *)dense_tc<64>;
-    const cudaError_t e = ensure_dyn_smem(kernel, (int)smem);
-    if (e != cudaSuccess)
-        return e;
-    return D == 128 ? launch_ex(dense_tc<128>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a, box)
-                    : launch_ex(dense_tc<64>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a, box);
+    return D == 128 ? launch_tc<128, 5>(qmap, kmap, vmap, a, box, grid, st)
+                    : launch_tc<64, 8>(qmap, kmap, vmap, a, box, grid, st);
 }
 
 }  // namespace ts

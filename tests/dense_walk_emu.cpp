@@ -29,7 +29,17 @@ using std::max;
 using std::min;
 typedef uint16_t __nv_bfloat16;
 
+struct DenseArgs;
+static int dense_next_seq(const DenseArgs &a, int b);
 #include "walk.inc"
+
+// (the device's takes 32 sequences a round trip)
+static int dense_next_seq(const DenseArgs &a, int b)
+{
+    while (b < a.B && seq_items(a, a.q_off[b + 1] - a.q_off[b]) == 0)
+        ++b;
+    return b;
+}
 
 int main()
 {
@@ -74,7 +84,7 @@ int main()
             w.begin(a, start.data());
             pieces[c] = w.piece(a);
             DenseItem it;
-            while (w.next(a, start.data(), it)) {
+            while (w.next(a, it)) {
                 ok &= it.kt0 < it.kt1 && it.off == so[it.b] && it.q_row == qo[it.b] + (int64_t)it.t * a.TT;
                 ok &= it.n == so[it.b + 1] - so[it.b];
                 ok &= it.first_pos == it.n - (qo[it.b + 1] - qo[it.b]) + (int64_t)it.t * a.TT;

@@ -284,13 +284,21 @@ def test_binding_refuses_host_tensors_and_wrong_types_of_new_tokens():
     with pytest.raises(ValueError, match="GPU only"):
         ts.ts_extend_pages(i64, i64, 16, torch.zeros(1, dtype=torch.int32), 1, torch.zeros((1, 1), dtype=torch.int32),
                            torch.zeros(2, dtype=torch.int64), torch.zeros(2, dtype=torch.int64), i64, i64)
-    dev = torch.device("cpu")
     rows = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU only"):
-        ts._token_rows("q", rows, 2, 64, dev)
+        ts._token_rows("q", rows, 2, 64, 0)
     with pytest.raises(TypeError, match="torch tensor"):
-        ts._token_rows("q", [1.0], 2, 64, dev)
+        ts._token_rows("q", [1.0], 2, 64, 0)
     with pytest.raises(ValueError, match="GPU only"):
-        ts._on_device("slots", i64, torch.int64, dev)
+        ts._address("slots", i64, torch.int64, 0, (1,))
+    # (a host tensor's device is -1: the checks behind the device's)
+    for t, dtype, shape in ((i64, torch.int32, (1,)), (rows[:, 0], torch.bfloat16, (4, 64)), (i64, torch.int64, (2,))):
+        with pytest.raises((TypeError, ValueError), match="must"):
+            ts._address("t", t, dtype, -1, shape)
+    for t in (rows.float(), rows[0], rows[:, :1], rows.transpose(0, 1), rows[:, :, ::2]):
+        with pytest.raises((TypeError, ValueError), match="must"):
+            ts._token_rows("t", t, 2, 64, -1)
+    assert ts._token_rows("t", rows, 2, 64, -1) == 128
+    assert ts._token_rows("t", torch.zeros((4, 6, 64), dtype=torch.bfloat16)[:, 2:4], 2, 64, -1) == 384
     with pytest.raises(ValueError, match="entries"):
         ts._host_offsets([0, 1, 2], 1)

@@ -16,7 +16,7 @@ HARNESS = os.path.join(ROOT, "tests", "dense_walk_emu.cpp")
 
 def walk_source(src: str) -> str:
     """From the tile's constant to the end of the walk, without the block-wide
-    prefix sum (the harness fills that table itself)."""
+    prefix sum and the warp-wide search (the harness has its own)."""
     start = src.index("constexpr int kDenseTile")
     line = src.index("// The line's sequence boundaries in start")
     place = src.index("// A place on the line")
