@@ -13,84 +13,28 @@ namespace {
 
 constexpr int kMergeWarps = 8;
 
-// An item that blocks c, c+1, ... shared: block c holds its beginning (slot
-// 2c + 1), each further one the rest of its part (slot 2q), up to the first
-// that is not wholly inside the item.  With (m_p, l_p, O_p) a piece's maximum
-// in base 2, sum and weighted sum, M = max m_p:
-//   O = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
-// in piece order.  One warp a row, grid (blocks of the main kernel - 1, row
-// groups); blocks whose c ends at an item's end return.
+// The shared items of dense_tc: a block of this kernel for each block of that
+// one and group of rows; those whose block begins no shared item return.  One
+// warp a row.  (dense_one's blocks join theirs themselves, a few rows an item;
+// up to 256 rows of many pieces want more warps than the last block has.)
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-dense_merge(const DenseArgs a, int blocks, int slot_rows)
+dense_merge(const DenseArgs a, int blocks)
 {
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int PS = D + 4, C = D / 32;
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const DensePiece p = a.pieces[c];
     if (!(p.flags & kPieceHead))
         return;
-    int last = c + 1;
-    for (;; last += 32) {
-        const bool ends = last + lane >= blocks || !(a.pieces[last + lane].flags & kPieceThrough);
-        const uint32_t vote = __ballot_sync(0xffffffffu, ends);
-        if (vote) {
-            last = min(last + __ffs(vote) - 1, blocks - 1);
-            break;
-        }
-    }
-    const int count = last - c + 1, T = kStreamRows / a.G;
+    const DenseChain ch = dense_chain(a, c, true, blocks, lane);
+    const int T = kStreamRows / a.G;
     const int64_t f = a.q_off[p.b + 1] - a.q_off[p.b], q_row = a.q_off[p.b] + (int64_t)p.t * a.TT;
     const int tokens = (int)min((int64_t)a.TT, f - (int64_t)p.t * a.TT);
     for (int i = blockIdx.y * kMergeWarps + warp; i < tokens * a.G; i += gridDim.y * kMergeWarps) {
         const int token = i / a.G, head = i - token * a.G;
-        const int row = token / T * kStreamRows + (token % T) * a.G + head;
-        auto piece = [&](int u) {
-            return a.part + ((int64_t)(u == 0 ? 2 * c + 1 : 2 * (c + u)) * slot_rows + row) * PS;
-        };
-        auto holds = [&](int u) { return u == 0 || !(a.pieces[c + u].flags & kPieceEmpty); };
-        float M = -INFINITY;
-        for (int u = lane; u < count; u += 32)
-            if (holds(u))
-                M = fmaxf(M, piece(u)[D]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float L = 0.0f, acc[C];
-#pragma unroll
-        for (int e = 0; e < C; ++e)
-            acc[e] = 0.0f;
-        for (int u0 = 0; u0 < count; u0 += 32) {
-            float w = 0.0f, l = 0.0f;
-            if (u0 + lane < count && holds(u0 + lane)) {
-                const float2 ml = *reinterpret_cast<const float2 *>(piece(u0 + lane) + D);
-                // (a maximum of -inf with a sum: every score seen was NaN)
-                w = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - M);
-                l = ml.y * w;
-            }
-#pragma unroll 4
-            for (int j = 0; j < min(32, count - u0); ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-                L += __shfl_sync(0xffffffffu, l, j);
-                if (wj != 0.0f) {
-                    const float *src = piece(u0 + j) + lane * C;
-#pragma unroll
-                    for (int e = 0; e < C; e += 2) {
-                        const float2 x = *reinterpret_cast<const float2 *>(src + e);
-                        acc[e] += wj * x.x;
-                        acc[e + 1] += wj * x.y;
-                    }
-                }
-            }
-        }
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const int64_t at = (q_row + token) * a.Hq + p.g * a.G + head;
-#pragma unroll
-        for (int e = 0; e < C; e += 2)
-            *reinterpret_cast<uint32_t *>(a.out + at * D + lane * C + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        if (a.lse != nullptr && lane == 0)
-            a.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2f;
+        dense_join_row<D>(a, ch, token / T * kStreamRows + (token % T) * a.G + head,
+                          (q_row + token) * a.Hq + p.g * a.G + head, lane);
     }
 }
 
@@ -104,7 +48,11 @@ cudaError_t launch_dense_one(const CUtensorMap &kmap, const CUtensorMap &vmap, c
 void plan_dense(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp)
 {
     const Plan &p = dp->p;
-    size_t o = 256;                            // the control block
+    // the control block, then the counters of the shared items (in one place
+    // for every shape, so that a workspace may serve several)
+    size_t o = 256;
+    dp->off_counts = o;
+    o = align_up(o + sizeof(uint32_t) * 8 * (size_t)p.sms, 256);
     for (int one = 0; one < 2; ++one) {
         DenseLaunch &w = dp->launch[one];
         w.TT = one ? 1 : 2 * (kStreamRows / p.G);
@@ -187,14 +135,17 @@ ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, 
         a.TT = w.TT;
         a.single = one;
         a.split = w.split;
+        a.inv_grid = 1.0 / w.grid;
+        a.slot_rows = w.slot_rows;
+        a.counts = reinterpret_cast<uint32_t *>(ws + dp.off_counts);
         a.pieces = reinterpret_cast<DensePiece *>(ws + w.off_pieces);
         a.part = reinterpret_cast<float *>(ws + w.off_part);
         cudaError_t e = one ? launch_dense_one(kmap, vmap, a, p.D, box, w.grid, st)
                             : launch_dense_tc(qmap, kmap, vmap, a, p.D, box, w.grid, st);
-        if (e == cudaSuccess && w.split && w.grid > 1) {
-            const dim3 grid(w.grid - 1, one ? (p.G + kMergeWarps - 1) / kMergeWarps : 8);
-            e = p.D == 128 ? launch_ex(dense_merge<128>, grid, dim3(kMergeWarps * 32), 0, st, 1, a, w.grid, w.slot_rows)
-                           : launch_ex(dense_merge<64>, grid, dim3(kMergeWarps * 32), 0, st, 1, a, w.grid, w.slot_rows);
+        if (e == cudaSuccess && !one && w.split && w.grid > 1) {
+            const dim3 grid(w.grid - 1, 8);
+            e = p.D == 128 ? launch_ex(dense_merge<128>, grid, dim3(kMergeWarps * 32), 0, st, 1, a, w.grid)
+                           : launch_ex(dense_merge<64>, grid, dim3(kMergeWarps * 32), 0, st, 1, a, w.grid);
         }
         if (e != cudaSuccess) {
             set_error("dense attention launch: %s", cudaGetErrorString(e));

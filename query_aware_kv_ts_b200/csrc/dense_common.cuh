@@ -46,6 +46,9 @@ struct DenseArgs {
     int TT;               // query tokens per item
     int single;           // 1: the sequences with one query token, 0: those with more
     int split;            // 0: parts end between items only
+    double inv_grid;      // 1 / blocks
+    int slot_rows;        // rows of one partial result
+    uint32_t *counts;     // [grid][8], zero between calls: tiles done of the items that blocks share
     float scale, scale_log2;
     // paged cache (page_table != null): token i of sequence b is pool row
     // page_table[b * pt_stride + (i >> page_shift)] << page_shift | (i & (page - 1))
@@ -62,6 +65,7 @@ struct DenseItem {
     int32_t slot;              // -1: the whole item; else its piece's place in the partial results
     int64_t q_row;             // its first query row
     int64_t off, n, first_pos; // the sequence's first row and length; position of its first query token
+    int32_t counter;           // for the shared items, a number below gridDim.x of each one's own
 };
 
 // Cost of an item beside its tokens, in tokens: measured start and end of an item.
@@ -78,44 +82,62 @@ __device__ __forceinline__ int64_t items_cost(const DenseArgs &a, int64_t base, 
     return t * (base + kItemCost) + (int64_t)a.TT * (t * (t + 1) / 2);
 }
 
-// The line's sequence boundaries in start[0..B] (shared memory; only begin()
-// below reads them, before the block's first load, so they may lie where the
-// tiles will).  Every thread of the block calls it.
-__device__ __forceinline__ void dense_line(const DenseArgs &a, int64_t *start, int64_t *s_warp)
+// The offsets and the line's sequence boundaries, [B + 1] each in shared
+// memory, for DenseWalk::begin: it is done before the block's first load, so
+// they may lie where the tiles will.
+struct DenseTables {
+    int64_t *start, *seq_off, *q_off;
+};
+constexpr size_t kDenseTableBytes = 3 * sizeof(int64_t) * (kMaxBatch + 1);
+__device__ __forceinline__ DenseTables dense_tables(void *p)
+{
+    int64_t *t = static_cast<int64_t *>(p);
+    return {t, t + kMaxBatch + 1, t + 2 * (kMaxBatch + 1)};
+}
+
+// Fills the tables, one round trip to memory.  Every thread of the block
+// calls it.
+__device__ __forceinline__ void dense_line(const DenseArgs &a, const DenseTables &tab, int64_t *s_warp)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int b = tid; b <= a.B; b += blockDim.x) {
+        tab.seq_off[b] = __ldcg(a.seq_off + b);
+        tab.q_off[b] = __ldcg(a.q_off + b);
+    }
+    __syncthreads();
     const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
     int64_t sum = 0;
     for (int u = 0; u < per; ++u) {
         const int b = tid * per + u;
         if (b >= a.B)
             break;
-        const int64_t n = __ldcg(a.seq_off + b + 1) - __ldcg(a.seq_off + b);
-        const int64_t f = __ldcg(a.q_off + b + 1) - __ldcg(a.q_off + b);
+        const int64_t n = tab.seq_off[b + 1] - tab.seq_off[b], f = tab.q_off[b + 1] - tab.q_off[b];
         sum += a.Hkv * items_cost(a, n > f ? n - f : 0, seq_items(a, f));
-        start[b + 1] = sum;
+        tab.start[b + 1] = sum;
     }
     int64_t incl = sum;
+    if (a.B > per) {                                 // more than one thread has sequences
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += y;
-    }
-    if (lane == 31)
-        s_warp[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - sum;
-    for (int w = 0; w < warp; ++w)
-        before += s_warp[w];
-    for (int u = 0; u < per; ++u) {
-        const int b = tid * per + u;
-        if (b >= a.B)
-            break;
-        start[b + 1] += before;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        if (lane == 31)
+            s_warp[warp] = incl;
+        __syncthreads();
+        int64_t before = incl - sum;
+        for (int w = 0; w < warp; ++w)
+            before += s_warp[w];
+        for (int u = 0; u < per; ++u) {
+            const int b = tid * per + u;
+            if (b >= a.B)
+                break;
+            tab.start[b + 1] += before;
+        }
     }
     if (tid == 0)
-        start[0] = 0;
+        tab.start[0] = 0;
     __syncthreads();
 }
 
@@ -137,7 +159,8 @@ __device__ __forceinline__ int dense_next_seq(const DenseArgs &a, int b)
 struct DensePlace {
     int32_t b, g, t, cut;
     int32_t tiles;            // of the item
-    int64_t f, n;
+    int64_t f, n, off, q0;    // of the sequence: query tokens, tokens, first token row, first query row
+    int64_t line;             // the sequence's beginning on the line
 };
 
 __device__ __forceinline__ void dense_item_at(const DenseArgs &a, DensePlace &p)
@@ -148,8 +171,15 @@ __device__ __forceinline__ void dense_item_at(const DenseArgs &a, DensePlace &p)
 
 __device__ __forceinline__ void dense_load_seq(const DenseArgs &a, DensePlace &p)
 {
-    p.n = __ldcg(a.seq_off + p.b + 1) - __ldcg(a.seq_off + p.b);
-    p.f = __ldcg(a.q_off + p.b + 1) - __ldcg(a.q_off + p.b);
+    p.off = __ldcg(a.seq_off + p.b);
+    p.n = __ldcg(a.seq_off + p.b + 1) - p.off;
+    p.q0 = __ldcg(a.q_off + p.b);
+    p.f = __ldcg(a.q_off + p.b + 1) - p.q0;
+}
+
+__device__ __forceinline__ int64_t dense_head_cost(const DenseArgs &a, const DensePlace &p)
+{
+    return items_cost(a, p.n > p.f ? p.n - p.f : 0, seq_items(a, p.f));
 }
 
 __device__ __forceinline__ void dense_next_item(const DenseArgs &a, DensePlace &p)
@@ -159,6 +189,7 @@ __device__ __forceinline__ void dense_next_item(const DenseArgs &a, DensePlace &
         p.t = 0;
         if (++p.g == a.Hkv) {
             p.g = 0;
+            p.line += a.Hkv * dense_head_cost(a, p);   // (sequences without items take no room on it)
             p.b = dense_next_seq(a, p.b + 1);
             if (p.b < a.B)
                 dense_load_seq(a, p);
@@ -168,12 +199,28 @@ __device__ __forceinline__ void dense_next_item(const DenseArgs &a, DensePlace &
         dense_item_at(a, p);
 }
 
-__device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int64_t *start, int64_t x)
+// Where part c begins on the line (part gridDim.x: its end).
+__device__ __forceinline__ int64_t dense_part(const DenseArgs &a, int64_t total, int c)
 {
+    return c >= (int)gridDim.x ? total : (int64_t)((double)total * c * a.inv_grid);
+}
+
+__device__ __forceinline__ void dense_table_seq(const DenseTables &tab, DensePlace &p)
+{
+    p.off = tab.seq_off[p.b];
+    p.n = tab.seq_off[p.b + 1] - p.off;
+    p.q0 = tab.q_off[p.b];
+    p.f = tab.q_off[p.b + 1] - p.q0;
+    p.line = tab.start[p.b];
+}
+
+__device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const DenseTables &tab, int64_t x)
+{
+    const int64_t *start = tab.start;
     DensePlace p;
     p.b = a.B;
     p.g = p.t = p.cut = p.tiles = 0;
-    p.f = p.n = 0;
+    p.f = p.n = p.off = p.q0 = p.line = 0;
     if (x >= start[a.B])
         return p;
     int lo = 0, hi = a.B;                      // start[lo] <= x < start[hi]
@@ -185,12 +232,14 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int
             hi = mid;
     }
     p.b = lo;
-    dense_load_seq(a, p);
+    dense_table_seq(tab, p);
     const int64_t base = p.n > p.f ? p.n - p.f : 0, items = seq_items(a, p.f);
     const int64_t head = items_cost(a, base, items);
     int64_t rem = x - start[lo];
-    p.g = (int32_t)(rem / head);
-    rem -= p.g * head;
+    while (rem >= head) {                      // at most 7 times
+        rem -= head;
+        ++p.g;
+    }
     int64_t t0 = 0, t1 = items;                // items_cost(t0) <= rem < items_cost(t1)
     while (t1 - t0 > 1) {
         const int64_t mid = (t0 + t1) >> 1;
@@ -203,8 +252,9 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int
     rem -= items_cost(a, base, t0);
     dense_item_at(a, p);
     if (a.split) {
-        const int64_t c = (rem - kItemCost + kDenseTile / 2) / kDenseTile;
-        p.cut = (int32_t)(c < 0 ? 0 : (c < p.tiles ? c : p.tiles));
+        const int32_t c = rem < kItemCost - kDenseTile / 2 ? 0
+                              : (int32_t)((rem - kItemCost + kDenseTile / 2) / kDenseTile);
+        p.cut = c < p.tiles ? c : p.tiles;
         if (p.tiles >= 8) {                    // no piece of a single tile
             if (p.cut < 2)
                 p.cut = 0;
@@ -214,8 +264,22 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int
     } else {
         p.cut = 2 * rem < base + (t0 + 1) * a.TT + kItemCost ? 0 : p.tiles;
     }
-    if (p.cut == p.tiles)
-        dense_next_item(a, p);
+    if (p.cut == p.tiles) {                    // the next item's beginning
+        p.cut = 0;
+        if (++p.t == items) {
+            p.t = 0;
+            if (++p.g == a.Hkv) {
+                p.g = 0;
+                do {
+                    ++p.b;
+                } while (p.b < a.B && start[p.b + 1] == start[p.b]);
+                if (p.b < a.B)
+                    dense_table_seq(tab, p);
+            }
+        }
+        if (p.b < a.B)
+            dense_item_at(a, p);
+    }
     return p;
 }
 
@@ -223,12 +287,13 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const int
 // its part.  All lanes of a warp walk alike.
 struct DenseWalk {
     DensePlace at, end;
+    int64_t total;
 
-    __device__ __forceinline__ void begin(const DenseArgs &a, const int64_t *start)
+    __device__ __forceinline__ void begin(const DenseArgs &a, const DenseTables &tab)
     {
-        const int64_t total = start[a.B], c = blockIdx.x, n = gridDim.x;
-        at = dense_locate(a, start, total / n * c + total % n * c / n);
-        end = dense_locate(a, start, total / n * (c + 1) + total % n * (c + 1) / n);
+        total = tab.start[a.B];
+        at = dense_locate(a, tab, dense_part(a, total, (int)blockIdx.x));
+        end = dense_locate(a, tab, dense_part(a, total, (int)blockIdx.x + 1));
     }
     __device__ __forceinline__ bool same_item() const { return at.b == end.b && at.g == end.g && at.t == end.t; }
     // For dense_merge; call it before next().
@@ -259,9 +324,22 @@ struct DenseWalk {
         it.tiles = at.tiles;
         it.tokens = (int32_t)min((int64_t)a.TT, at.f - (int64_t)at.t * a.TT);
         it.slot = it.kt0 == 0 && it.kt1 == at.tiles ? -1 : 2 * (int32_t)blockIdx.x + (it.kt0 == 0 ? 1 : 0);
-        it.off = __ldcg(a.seq_off + at.b);
-        it.q_row = __ldcg(a.q_off + at.b) + (int64_t)at.t * a.TT;
+        it.off = at.off;
+        it.q_row = at.q0 + (int64_t)at.t * a.TT;
         it.n = at.n;
+        it.counter = 0;
+        if (it.slot >= 0) {
+            // the part in which the item begins: an item that a part's end
+            // cuts is the last to begin in its part
+            const int64_t x =
+                at.line + at.g * dense_head_cost(a, at) + items_cost(a, at.n > at.f ? at.n - at.f : 0, at.t);
+            int c = (int)((double)x * (double)gridDim.x / (double)total);
+            while (dense_part(a, total, c) > x)
+                --c;
+            while (dense_part(a, total, c + 1) <= x)
+                ++c;
+            it.counter = c;
+        }
         it.first_pos = at.n - at.f + (int64_t)at.t * a.TT;
         if (last)
             at.cut = end.cut;                                // next() ends here
@@ -390,8 +468,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32
 // shorter pages one box per page and half, each issued by its own lane.  An
 // item with b < 0 ends the line.
 template <int D, int NS, bool QL, int MAXNS>
-__device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> &r, const int64_t *start,
-                                           uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap, int box,
+__device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> &r, uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap, int box,
                                            int lane, const QueryLoad<D> &q)
 {
     const int T = kStreamRows / a.G;
@@ -400,9 +477,9 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     const bool mine = lane < npp * (D / 64);
     const int64_t oob = a.pool_pages << a.page_shift;   // past the pool: reads zeros
     DenseWalk w;
-    w.begin(a, start);
+    w.begin(a, dense_tables(ring));
     __syncwarp();
-    fence_proxy_async_smem();                        // start's reads are done: tiles may go over it
+    fence_proxy_async_smem();                        // the tables are read: tiles may go over them
     if (lane == 0)
         a.pieces[blockIdx.x] = w.piece(a);
     uint32_t n = 0;                                  // tiles loaded (K and V count one each)
@@ -482,6 +559,99 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
         if (QL && k > 0)
             (void)mbar_wait_bounded(q.full, (k - 1) & 1, kSpinLimit);
     }
+}
+
+// The blocks that share an item: head begins it (slot 2 head + 1), each
+// further one up to last has the rest of its part (slot 2 q; some hold none).
+struct DenseChain {
+    int head, last;
+};
+
+// Whole warp: the item that block c begins (begins) or goes on with.
+__device__ __forceinline__ DenseChain dense_chain(const DenseArgs &a, int c, bool begins, int blocks, int lane)
+{
+    DenseChain ch = {c, c};
+    auto flags = [&](int q) { return __ldcg(&a.pieces[q].flags); };
+    if (!begins)
+        for (int q = c - 1;; q -= 32) {
+            const uint32_t vote = __ballot_sync(0xffffffffu, q - lane < 0 || (flags(q - lane) & kPieceHead));
+            if (vote) {
+                ch.head = max(q - (__ffs(vote) - 1), 0);
+                break;
+            }
+        }
+    if (begins || (flags(c) & kPieceThrough))
+        for (int q = c + 1;; q += 32) {
+            const uint32_t vote =
+                __ballot_sync(0xffffffffu, q + lane >= blocks || !(flags(q + lane) & kPieceThrough));
+            if (vote) {
+                ch.last = min(q + __ffs(vote) - 1, blocks - 1);
+                break;
+            }
+        }
+    return ch;
+}
+
+// Whole warp: one row of a shared item.  With (m_p, l_p, O_p) a piece's
+// maximum in base 2, sum and weighted sum, and M = max m_p:
+//   O = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
+// in piece order, to row `at` (query row x head) of the output.
+template <int D>
+__device__ __forceinline__ void dense_join_row(const DenseArgs &a, const DenseChain &ch, int row, int64_t at, int lane)
+{
+    constexpr int PS = D + 4, C = D / 32;
+    const int count = ch.last - ch.head + 1;
+    auto piece = [&](int u) {
+        return a.part + ((int64_t)(u == 0 ? 2 * ch.head + 1 : 2 * (ch.head + u)) * a.slot_rows + row) * PS;
+    };
+    auto holds = [&](int u) { return u == 0 || !(__ldcg(&a.pieces[ch.head + u].flags) & kPieceEmpty); };
+    float M = -INFINITY;
+    for (int u = lane; u < count; u += 32)
+        if (holds(u))
+            M = fmaxf(M, __ldcg(piece(u) + D));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.0f, acc[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e)
+        acc[e] = 0.0f;
+    for (int u0 = 0; u0 < count; u0 += 32) {
+        float w = 0.0f, l = 0.0f;
+        if (u0 + lane < count && holds(u0 + lane)) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(piece(u0 + lane) + D));
+            // (a maximum of -inf with a sum: every score seen was NaN)
+            w = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - M);
+            l = ml.y * w;
+        }
+        const int n = min(32, count - u0);
+        for (int j0 = 0; j0 < n; j0 += 8) {
+            float2 x[8][C / 2];
+            float wj[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {            // eight pieces' rows in flight
+                wj[j] = __shfl_sync(0xffffffffu, w, j0 + j);
+                L += __shfl_sync(0xffffffffu, l, j0 + j);
+#pragma unroll
+                for (int e = 0; e < C / 2; ++e)
+                    x[j][e] = wj[j] != 0.0f ? __ldcg(reinterpret_cast<const float2 *>(piece(u0 + j0 + j) + lane * C) + e)
+                                            : make_float2(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < C / 2; ++e) {
+                    acc[2 * e] += wj[j] * x[j][e].x;
+                    acc[2 * e + 1] += wj[j] * x[j][e].y;
+                }
+        }
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int e = 0; e < C; e += 2)
+        *reinterpret_cast<uint32_t *>(a.out + at * D + lane * C + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2f;
 }
 
 }  // namespace ts

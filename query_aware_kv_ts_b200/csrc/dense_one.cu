@@ -56,7 +56,8 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
         if (b < 0)
             return;
         const int g = sh.ring.item[slot].g, kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
-        const int part_slot = sh.ring.item[slot].slot;
+        const int part_slot = sh.ring.item[slot].slot, counter = sh.ring.item[slot].counter;
+        const int tiles = sh.ring.item[slot].tiles;
         const int64_t q_row = sh.ring.item[slot].q_row, len = sh.ring.item[slot].n;
         uint32_t qa[D / 16][4];
         const __nv_bfloat16 *q = a.q + q_row * a.q_st + (int64_t)g * a.G * D;
@@ -73,17 +74,13 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.ring.item_empty[slot]);
-        // weighted sums: rows r0 and r0 + 8; the remainders' are rows r0 + 8
-        // up to 8 heads, and o2 above
-        float o[D / 8][4], o2[WIDE ? D / 8 : 1][4];
+        // weighted sums: rows r0 and r0 + 8 (up to 8 heads, the remainders')
+        float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 o[i][e] = 0.0f;
-                if (WIDE)
-                    o2[i][e] = 0.0f;
-            }
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         for (int kt = kt0; kt < kt1; ++kt, n += 2) {
             const int left = (int)min(len - (int64_t)kt * kDenseTile - warp * 16, (int64_t)16);   // tokens of the slab
@@ -134,10 +131,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                     for (int i = 0; i < D / 8; ++i) {
                         o[i][2 * e] *= f;
                         o[i][2 * e + 1] *= f;
-                        if (WIDE) {
-                            o2[i][2 * e] *= f;
-                            o2[i][2 * e + 1] *= f;
-                        } else {
+                        if (!WIDE) {
                             o[i][2] *= f;
                             o[i][3] *= f;
                         }
@@ -152,8 +146,18 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                 for (int nb = 0; nb < 2; ++nb) {
                     const float p0 = ex2(fmaf(s[nb][2 * e], c, -mc)), p1 = ex2(fmaf(s[nb][2 * e + 1], c, -mc));
                     l[e] += p0 + p1;
-                    hi[nb][e] = pack_bf16(p0, p1);
-                    lo[nb][e] = pack_bf16(p0 - bf16_lo(hi[nb][e]), p1 - bf16_hi(hi[nb][e]));
+                    if (WIDE) {
+                        // both parts go into one sum: cut off, not rounded,
+                        // the remainder has the weight's sign, and at least
+                        // the smallest normal number keeps 0 times an
+                        // infinity of V out of it
+                        hi[nb][e] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                        lo[nb][e] = pack_bf16(fmaxf(p0 - bf16_lo(hi[nb][e]), fminf(p0, 1.1754944e-38f)),
+                                              fmaxf(p1 - bf16_hi(hi[nb][e]), fminf(p1, 1.1754944e-38f)));
+                    } else {
+                        hi[nb][e] = pack_bf16(p0, p1);
+                        lo[nb][e] = pack_bf16(p0 - bf16_lo(hi[nb][e]), p1 - bf16_hi(hi[nb][e]));
+                    }
                 }
             }
             // ---- O += P V ----
@@ -178,9 +182,9 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                 b3 &= keep1;
                 if (WIDE) {
                     mma_16816(o[i], hi[0][0], hi[0][1], hi[1][0], hi[1][1], b0, b1);
-                    mma_16816(o2[i], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b0, b1);
+                    mma_16816(o[i], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b0, b1);
                     mma_16816(o[i + 1], hi[0][0], hi[0][1], hi[1][0], hi[1][1], b2, b3);
-                    mma_16816(o2[i + 1], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b2, b3);
+                    mma_16816(o[i + 1], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b2, b3);
                 } else {
                     mma_16816(o[i], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b0, b1);
                     mma_16816(o[i + 1], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b2, b3);
@@ -205,8 +209,8 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                 float x[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float y = o[i][2 * e + u], rest = WIDE ? o2[i][2 * e + u] : o[i][2 + u];
-                    x[u] = isinf(y) ? y : y + rest;
+                    const float y = o[i][2 * e + u];
+                    x[u] = WIDE || isinf(y) ? y : y + o[i][2 + u];
                 }
                 *reinterpret_cast<float2 *>(row + i * 8 + c0) = make_float2(x[0], x[1]);
             }
@@ -254,12 +258,32 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                 if (a.lse != nullptr && lane == 0)
                     a.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * kLn2f;
             } else {
-                float *dst = a.part + ((int64_t)part_slot * 16 + row) * PS;
+                float *dst = a.part + ((int64_t)part_slot * a.slot_rows + row) * PS;
 #pragma unroll
                 for (int i = 0; i < D / 32; i += 2)
                     *reinterpret_cast<float2 *>(dst + lane * (D / 32) + i) = make_float2(acc[i], acc[i + 1]);
                 if (lane == 0)
                     *reinterpret_cast<float2 *>(dst + D) = make_float2(M, L);
+            }
+        }
+        // A shared item's rows are joined by whichever block's warp comes last
+        // (the sum is taken in piece order, whoever that is): each adds its
+        // tiles to the rows' counter and goes on.
+        if (part_slot >= 0 && warp < a.G) {
+            uint32_t *count = a.counts + counter * 8 + warp;
+            __threadfence();
+            __syncwarp();
+            uint32_t before = 0;
+            if (lane == 0)
+                before = atomicAdd(count, (uint32_t)(kt1 - kt0));
+            before = __shfl_sync(0xffffffffu, before, 0);
+            if (before + (uint32_t)(kt1 - kt0) == (uint32_t)tiles) {
+                __threadfence();
+                const DenseChain ch = dense_chain(a, (int)blockIdx.x, kt0 == 0, (int)gridDim.x, lane);
+                for (int row = warp; row < a.G; row += kOneWarps)
+                    dense_join_row<D>(a, ch, row, q_row * a.Hq + g * a.G + row, lane);
+                if (lane == 0)
+                    *count = 0u;                     // as the next call finds it
             }
         }
         __syncwarp();
@@ -277,7 +301,6 @@ dense_one(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     __shared__ OneShared sh;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
     float *join = reinterpret_cast<float *>(ring + kOneStages<D, WIDE> * kTileBytes<D>);
-    int64_t *start = reinterpret_cast<int64_t *>(ring);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         sh.ring.init(kOneStages<D, WIDE>, kOneWarps, kOneWarps);
@@ -289,10 +312,10 @@ dense_one(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
         tma_prefetch_desc(lane ? &vmap : &kmap);
     pdl_wait();
     pdl_launch_dependents();
-    dense_line(a, start, sh.s_warp);                 // ends with a barrier
+    dense_line(a, dense_tables(ring), sh.s_warp);                 // ends with a barrier
     if (warp == kOneWarps) {
         const QueryLoad<D> none = {};
-        load_items<D, kOneStages<D, WIDE>, false>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, none);
+        load_items<D, kOneStages<D, WIDE>, false>(a, sh.ring, ring, &kmap, &vmap, box, lane, none);
     } else {
         attend_items<D, WIDE>(a, sh, smem_u32(ring), join, warp, lane);
     }

@@ -182,7 +182,7 @@ __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &
         const int token = (quad + u) / a.G, head = (quad + u) - token * a.G;
         live[u] = token < tokens;
         base[u] = whole ? ((it.q_row + stream * T + token) * a.Hq + it.g * a.G + head) * D
-                        : ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + quad + u) * (D + 4);
+                        : ((int64_t)it.slot * a.slot_rows + stream * kStreamRows + quad + u) * (D + 4);
     }
 #pragma unroll 1
     for (int x = 0; x < D; x += 32) {
@@ -238,7 +238,7 @@ __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &
     }
     const int token = r / a.G, head = r - token * a.G;
     if (token < tokens && !whole)
-        *reinterpret_cast<float2 *>(a.part + ((int64_t)it.slot * (2 * kStreamRows) + stream * kStreamRows + r) *
+        *reinterpret_cast<float2 *>(a.part + ((int64_t)it.slot * a.slot_rows + stream * kStreamRows + r) *
                                                  (D + 4) + D) = make_float2(mb, l);
     else if (token < tokens && a.lse != nullptr)
         a.lse[(it.q_row + stream * T + token) * a.Hq + it.g * a.G + head] =
@@ -602,7 +602,6 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
     uint8_t *sq = dyn_smem, *ring = sq + 2 * kStreamRows * D * 2;
     TcShared &sh = *reinterpret_cast<TcShared *>(ring + NS * kTileBytes<D>);
-    int64_t *start = reinterpret_cast<int64_t *>(ring);
     if (smem_u32(dyn_smem) & 1023u) {                // (the swizzle's atoms are 1024 bytes)
         if (threadIdx.x == 0)
             report_timeout(a.ctrl, kSiteDense);
@@ -630,7 +629,7 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
     pdl_wait();
     pdl_launch_dependents();
     tmem_fence_before();
-    dense_line(a, start, sh.s_warp);                 // ends with a barrier
+    dense_line(a, dense_tables(ring), sh.s_warp);                 // ends with a barrier
     tmem_fence_after();
 
     if (warp < kSoftmaxWarps) {
@@ -640,7 +639,7 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
         if (warp == kLoadWarp) {
             const QueryLoad<D> q = {&qmap, sq, &sh.q_full, &sh.q_empty, sh.bad};
-            load_items<D, NS, true>(a, sh.ring, start, ring, &kmap, &vmap, box, lane, q);
+            load_items<D, NS, true>(a, sh.ring, ring, &kmap, &vmap, box, lane, q);
         } else if (warp == kMmaWarp) {
             issue_products<D, NS>(a, sh, smem_u32(sq), smem_u32(ring), lane);
             // every MMA issued has completed before TMEM is released
@@ -667,7 +666,7 @@ static cudaError_t launch_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, c
                              const DenseArgs &a, int box, int grid, cudaStream_t st)
 {
     constexpr size_t smem = (size_t)2 * kStreamRows * D * 2 + (size_t)NS * kTileBytes<D> + sizeof(TcShared);
-    static_assert(smem <= 227 * 1024 && (kMaxBatch + 1) * 8 <= NS * kTileBytes<D>, "shared memory");
+    static_assert(smem <= 227 * 1024 && kDenseTableBytes <= NS * kTileBytes<D>, "shared memory");
     const cudaError_t e = ensure_dyn_smem((const void *)dense_tc<D, NS>, (int)smem);
     if (e != cudaSuccess)
         return e;

@@ -237,7 +237,7 @@ struct DensePlan {
     Plan p;
     int64_t rows;            // query tokens: q_offsets[B]
     DenseLaunch launch[2];   // [0] sequences of several query tokens, [1] of one
-    size_t total_bytes;      // workspace
+    size_t off_counts, total_bytes;   // workspace
 };
 // q_off: the host copy of the query rows' offsets.
 ts_status_t make_dense_plan(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp);

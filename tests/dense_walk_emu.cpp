@@ -23,6 +23,7 @@ static dim3 blockIdx, gridDim;
 #define __device__
 #define __forceinline__ inline
 #define __align__(x) alignas(x)
+constexpr int kMaxBatch = 1024;
 template <typename T>
 static T __ldcg(const T *p) { return *p; }
 using std::max;
@@ -71,9 +72,11 @@ int main()
             const int64_t n = so[b + 1] - so[b], f = qo[b + 1] - qo[b];
             start[b + 1] = start[b] + a.Hkv * items_cost(a, n > f ? n - f : 0, seq_items(a, f));
         }
+        a.inv_grid = 1.0 / gridDim.x;
+        const DenseTables tab = {start.data(), so.data(), qo.data()};
         using Key = std::tuple<int, int, int>;
         struct Part {
-            int kt0, kt1, slot, tiles, tokens;
+            int kt0, kt1, slot, tiles, tokens, counter;
         };
         std::map<Key, std::vector<Part>> got;
         std::vector<DensePiece> pieces(gridDim.x);
@@ -81,14 +84,14 @@ int main()
         for (unsigned c = 0; c < gridDim.x; ++c) {
             blockIdx.x = c;
             DenseWalk w;
-            w.begin(a, start.data());
+            w.begin(a, tab);
             pieces[c] = w.piece(a);
             DenseItem it;
             while (w.next(a, it)) {
                 ok &= it.kt0 < it.kt1 && it.off == so[it.b] && it.q_row == qo[it.b] + (int64_t)it.t * a.TT;
                 ok &= it.n == so[it.b + 1] - so[it.b];
                 ok &= it.first_pos == it.n - (qo[it.b + 1] - qo[it.b]) + (int64_t)it.t * a.TT;
-                got[Key(it.b, it.g, it.t)].push_back({it.kt0, it.kt1, it.slot, it.tiles, it.tokens});
+                got[Key(it.b, it.g, it.t)].push_back({it.kt0, it.kt1, it.slot, it.tiles, it.tokens, it.counter});
             }
         }
         size_t items = 0;
@@ -136,6 +139,14 @@ int main()
             joined.erase(e.first);
         }
         ok &= joined.empty();
+        // the shared items' counters: one for all pieces, of each item its own
+        std::map<int, Key> counters;
+        for (auto &e : got)
+            for (const Part &p : e.second)
+                if (p.slot >= 0)
+                    ok &= p.counter >= 0 && p.counter < (int)gridDim.x &&
+                          counters.emplace(p.counter, e.first).first->second == e.first &&
+                          p.counter == e.second[0].counter;
         ++cases;
         if (!ok && failures++ < 5)
             std::printf("failed: trial %d B %d Hkv %d G %d single %d split %d grid %u\n", trial, B, a.Hkv, a.G, a.single,

@@ -18,7 +18,7 @@ def walk_source(src: str) -> str:
     """From the tile's constant to the end of the walk, without the block-wide
     prefix sum and the warp-wide search (the harness has its own)."""
     start = src.index("constexpr int kDenseTile")
-    line = src.index("// The line's sequence boundaries in start")
+    line = src.index("// Fills the tables, one round trip")
     place = src.index("// A place on the line")
     end = src.index("// The K / V row of token i < n")
     return src[start:line] + src[place:end]

@@ -190,10 +190,11 @@ def test_more_queries_than_tokens():
 
 @pytest.mark.parametrize("page", [0, 16])
 @pytest.mark.parametrize("fresh", [1, 90, 333])
-def test_no_token_reaches_rows_that_do_not_see_it(fresh, page):
+@pytest.mark.parametrize("h_q", [14, 32])
+def test_no_token_reaches_rows_that_do_not_see_it(h_q, fresh, page):
     """NaN and infinities in K and V of one token: rows before it are as if it
     were not there, rows from it on are NaN or infinite in its channels."""
-    n, h_q, h_kv, d = 333, 14, 2, 128
+    n, h_kv, d = 333, 2, 128
     off, q_off, q, k, v = inputs([n, 50], [fresh, 50], h_q, h_kv, d, 31)
     clean = attend(k, v, off, q, q_off, h_q)
     at = n - fresh // 2 - 1
