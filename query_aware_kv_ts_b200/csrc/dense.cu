@@ -27,13 +27,12 @@ dense_merge(const DenseArgs a, int blocks)
     const DensePiece p = a.pieces[c];
     if (!(p.flags & kPieceHead))
         return;
-    const DenseChain ch = dense_chain(a, c, true, blocks, lane);
     const int T = kStreamRows / a.G;
     const int64_t f = a.q_off[p.b + 1] - a.q_off[p.b], q_row = a.q_off[p.b] + (int64_t)p.t * a.TT;
     const int tokens = (int)min((int64_t)a.TT, f - (int64_t)p.t * a.TT);
     for (int i = blockIdx.y * kMergeWarps + warp; i < tokens * a.G; i += gridDim.y * kMergeWarps) {
         const int token = i / a.G, head = i - token * a.G;
-        dense_join_row<D>(a, ch, token / T * kStreamRows + (token % T) * a.G + head,
+        dense_join_row<D>(a, p.b, p.g, p.t, c, blocks, token / T * kStreamRows + (token % T) * a.G + head,
                           (q_row + token) * a.Hq + p.g * a.G + head, lane);
     }
 }

@@ -82,65 +82,6 @@ __device__ __forceinline__ int64_t items_cost(const DenseArgs &a, int64_t base, 
     return t * (base + kItemCost) + (int64_t)a.TT * (t * (t + 1) / 2);
 }
 
-// The offsets and the line's sequence boundaries, [B + 1] each in shared
-// memory, for DenseWalk::begin: it is done before the block's first load, so
-// they may lie where the tiles will.
-struct DenseTables {
-    int64_t *start, *seq_off, *q_off;
-};
-constexpr size_t kDenseTableBytes = 3 * sizeof(int64_t) * (kMaxBatch + 1);
-__device__ __forceinline__ DenseTables dense_tables(void *p)
-{
-    int64_t *t = static_cast<int64_t *>(p);
-    return {t, t + kMaxBatch + 1, t + 2 * (kMaxBatch + 1)};
-}
-
-// Fills the tables, one round trip to memory.  Every thread of the block
-// calls it.
-__device__ __forceinline__ void dense_line(const DenseArgs &a, const DenseTables &tab, int64_t *s_warp)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int b = tid; b <= a.B; b += blockDim.x) {
-        tab.seq_off[b] = __ldcg(a.seq_off + b);
-        tab.q_off[b] = __ldcg(a.q_off + b);
-    }
-    __syncthreads();
-    const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
-    int64_t sum = 0;
-    for (int u = 0; u < per; ++u) {
-        const int b = tid * per + u;
-        if (b >= a.B)
-            break;
-        const int64_t n = tab.seq_off[b + 1] - tab.seq_off[b], f = tab.q_off[b + 1] - tab.q_off[b];
-        sum += a.Hkv * items_cost(a, n > f ? n - f : 0, seq_items(a, f));
-        tab.start[b + 1] = sum;
-    }
-    int64_t incl = sum;
-    if (a.B > per) {                                 // more than one thread has sequences
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += y;
-        }
-        if (lane == 31)
-            s_warp[warp] = incl;
-        __syncthreads();
-        int64_t before = incl - sum;
-        for (int w = 0; w < warp; ++w)
-            before += s_warp[w];
-        for (int u = 0; u < per; ++u) {
-            const int b = tid * per + u;
-            if (b >= a.B)
-                break;
-            tab.start[b + 1] += before;
-        }
-    }
-    if (tid == 0)
-        tab.start[0] = 0;
-    __syncthreads();
-}
-
 // The first sequence from b on that has items, B if none has.  Whole warp, 32
 // sequences a round trip.
 __device__ __forceinline__ int dense_next_seq(const DenseArgs &a, int b)
@@ -198,6 +139,12 @@ __device__ __forceinline__ void dense_next_item(const DenseArgs &a, DensePlace &
     if (p.b < a.B)
         dense_item_at(a, p);
 }
+
+// The offsets and the line's sequence boundaries, [B + 1] each, as
+// dense_locate reads them.
+struct DenseTables {
+    int64_t *start, *seq_off, *q_off;
+};
 
 // Where part c begins on the line (part gridDim.x: its end).
 __device__ __forceinline__ int64_t dense_part(const DenseArgs &a, int64_t total, int c)
@@ -283,18 +230,12 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const Den
     return p;
 }
 
-// The pieces of block c, one after another: next() is false at the end of
-// its part.  All lanes of a warp walk alike.
+// The pieces of a block's part from at to end, one after another: next() is
+// false at the end.  All lanes of a warp walk alike.
 struct DenseWalk {
     DensePlace at, end;
-    int64_t total;
+    int64_t total;                                          // the line's length
 
-    __device__ __forceinline__ void begin(const DenseArgs &a, const DenseTables &tab)
-    {
-        total = tab.start[a.B];
-        at = dense_locate(a, tab, dense_part(a, total, (int)blockIdx.x));
-        end = dense_locate(a, tab, dense_part(a, total, (int)blockIdx.x + 1));
-    }
     __device__ __forceinline__ bool same_item() const { return at.b == end.b && at.g == end.g && at.t == end.t; }
     // For dense_merge; call it before next().
     __device__ __forceinline__ DensePiece piece(const DenseArgs &a) const
@@ -348,6 +289,57 @@ struct DenseWalk {
         return true;
     }
 };
+
+// The block's part, found by one warp: the tables (in shared memory, where the
+// tiles will be) after one round trip to the offsets, 32 sequences at a time,
+// then both ends at once, one in lane 0 and one in lane 1.
+constexpr size_t kDenseTableBytes = 3 * sizeof(int64_t) * (kMaxBatch + 1) + 2 * sizeof(DensePlace);
+__device__ __forceinline__ void dense_begin(const DenseArgs &a, void *smem, int lane, DenseWalk &w)
+{
+    int64_t *t = static_cast<int64_t *>(smem);
+    const DenseTables tab = {t, t + kMaxBatch + 1, t + 2 * (kMaxBatch + 1)};
+    DensePlace *place = reinterpret_cast<DensePlace *>(t + 3 * (kMaxBatch + 1));
+    int64_t run = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        int64_t s0 = 0, s1 = 0, q0 = 0, q1 = 0;
+        if (b < a.B) {
+            s0 = __ldcg(a.seq_off + b);
+            s1 = __ldcg(a.seq_off + b + 1);
+            q0 = __ldcg(a.q_off + b);
+            q1 = __ldcg(a.q_off + b + 1);
+        }
+        const int64_t n = s1 - s0, f = q1 - q0;
+        int64_t cost = a.Hkv * items_cost(a, n > f ? n - f : 0, seq_items(a, f));
+        if (a.B > 1) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, cost, o);
+                if (lane >= o)
+                    cost += y;
+            }
+        }
+        if (b < a.B) {
+            tab.seq_off[b] = s0;
+            tab.q_off[b] = q0;
+            tab.seq_off[b + 1] = s1;
+            tab.q_off[b + 1] = q1;
+            tab.start[b + 1] = run + cost;
+        }
+        run += __shfl_sync(0xffffffffu, cost, 31);
+    }
+    if (lane == 0)
+        tab.start[0] = 0;
+    __syncwarp();
+    w.total = tab.start[a.B];
+    if (lane < 2)
+        place[lane] = dense_locate(a, tab, dense_part(a, w.total, (int)blockIdx.x + lane));
+    __syncwarp();
+    w.at = place[0];
+    w.end = place[1];
+    __syncwarp();
+}
 
 // The K / V row of token i < n of a sequence; -1 on a page outside the pool.
 __device__ __forceinline__ int64_t dense_row(const DenseArgs &a, int b, int64_t off, int64_t i)
@@ -477,8 +469,7 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     const bool mine = lane < npp * (D / 64);
     const int64_t oob = a.pool_pages << a.page_shift;   // past the pool: reads zeros
     DenseWalk w;
-    w.begin(a, dense_tables(ring));
-    __syncwarp();
+    dense_begin(a, ring, lane, w);
     fence_proxy_async_smem();                        // the tables are read: tiles may go over them
     if (lane == 0)
         a.pieces[blockIdx.x] = w.piece(a);
@@ -561,80 +552,73 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     }
 }
 
-// The blocks that share an item: head begins it (slot 2 head + 1), each
-// further one up to last has the rest of its part (slot 2 q; some hold none).
-struct DenseChain {
-    int head, last;
-};
-
-// Whole warp: the item that block c begins (begins) or goes on with.
-__device__ __forceinline__ DenseChain dense_chain(const DenseArgs &a, int c, bool begins, int blocks, int lane)
-{
-    DenseChain ch = {c, c};
-    auto flags = [&](int q) { return __ldcg(&a.pieces[q].flags); };
-    if (!begins)
-        for (int q = c - 1;; q -= 32) {
-            const uint32_t vote = __ballot_sync(0xffffffffu, q - lane < 0 || (flags(q - lane) & kPieceHead));
-            if (vote) {
-                ch.head = max(q - (__ffs(vote) - 1), 0);
-                break;
-            }
-        }
-    if (begins || (flags(c) & kPieceThrough))
-        for (int q = c + 1;; q += 32) {
-            const uint32_t vote =
-                __ballot_sync(0xffffffffu, q + lane >= blocks || !(flags(q + lane) & kPieceThrough));
-            if (vote) {
-                ch.last = min(q + __ffs(vote) - 1, blocks - 1);
-                break;
-            }
-        }
-    return ch;
-}
-
-// Whole warp: one row of a shared item.  With (m_p, l_p, O_p) a piece's
-// maximum in base 2, sum and weighted sum, and M = max m_p:
+// Whole warp: one row of an item that several blocks share.  The block that
+// begins it (the first from `from` on that says so) has its first piece (slot
+// 2 c + 1), each further block the rest of its part (slot 2 q; some hold
+// none), up to the first that is not wholly inside the item.  With (m_p, l_p,
+// O_p) a piece's maximum in base 2, sum and weighted sum, and M = max m_p:
 //   O = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
-// in piece order, to row `at` (query row x head) of the output.
+// in piece order, to row `at` (query row x head) of the output.  32 blocks'
+// pieces a round trip.
 template <int D>
-__device__ __forceinline__ void dense_join_row(const DenseArgs &a, const DenseChain &ch, int row, int64_t at, int lane)
+__device__ __forceinline__ void dense_join_row(const DenseArgs &a, int b, int g, int t, int from, int blocks, int row,
+                                               int64_t at, int lane)
 {
     constexpr int PS = D + 4, C = D / 32;
-    const int count = ch.last - ch.head + 1;
-    auto piece = [&](int u) {
-        return a.part + ((int64_t)(u == 0 ? 2 * ch.head + 1 : 2 * (ch.head + u)) * a.slot_rows + row) * PS;
-    };
-    auto holds = [&](int u) { return u == 0 || !(__ldcg(&a.pieces[ch.head + u].flags) & kPieceEmpty); };
-    float M = -INFINITY;
-    for (int u = lane; u < count; u += 32)
-        if (holds(u))
-            M = fmaxf(M, __ldcg(piece(u) + D));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.0f, acc[C];
+    int4 p;
+    uint32_t vote;
+    for (;; from += 32) {                            // (at the first place, but where parts hold less than a tile)
+        p = make_int4(-1, 0, 0, 0);
+        if (from + lane < blocks)
+            p = __ldcg(reinterpret_cast<const int4 *>(a.pieces + from + lane));
+        vote = __ballot_sync(0xffffffffu, (p.x == b && p.y == g && p.z == t && (p.w & kPieceHead)) ||
+                                              from + lane >= blocks);
+        if (vote)
+            break;
+    }
+    const int head = from + __ffs(vote) - 1;
+    float M = -INFINITY, L = 0.0f, acc[C];
 #pragma unroll
     for (int e = 0; e < C; ++e)
         acc[e] = 0.0f;
-    for (int u0 = 0; u0 < count; u0 += 32) {
-        float w = 0.0f, l = 0.0f;
-        if (u0 + lane < count && holds(u0 + lane)) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(piece(u0 + lane) + D));
-            // (a maximum of -inf with a sum: every score seen was NaN)
-            w = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - M);
-            l = ml.y * w;
+    for (int q0 = head; q0 < blocks;) {
+        // this round's pieces: the blocks q0 + lane of the item that hold some
+        const int q = q0 + lane;
+        const int flags = q < blocks ? __ldcg(&a.pieces[q].flags) : 0;
+        const uint32_t ends = __ballot_sync(0xffffffffu, q != head && !(flags & kPieceThrough));
+        const int count = ends ? __ffs(ends) : 32;   // the block that ends the item has the last
+        const bool holds = lane < count && q < blocks && (q == head || !(flags & kPieceEmpty));
+        const float *mine = a.part + ((int64_t)(q == head ? 2 * q + 1 : 2 * q) * a.slot_rows + row) * PS;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (holds)
+            ml = __ldcg(reinterpret_cast<const float2 *>(mine + D));
+        float top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top > M) {                               // the sums so far, relative to the new maximum
+            const float f = ex2(M - top);
+            M = top;
+            L *= f;
+#pragma unroll
+            for (int e = 0; e < C; ++e)
+                acc[e] *= f;
         }
-        const int n = min(32, count - u0);
-        for (int j0 = 0; j0 < n; j0 += 8) {
+        // (a maximum of -inf with a sum: every score seen was NaN)
+        const float w = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - M);
+        const float l = ml.y * w;
+        for (int j0 = 0; j0 < count; j0 += 8) {
             float2 x[8][C / 2];
             float wj[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {            // eight pieces' rows in flight
                 wj[j] = __shfl_sync(0xffffffffu, w, j0 + j);
                 L += __shfl_sync(0xffffffffu, l, j0 + j);
+                const int qj = q0 + j0 + j;
+                const float *src = a.part + ((int64_t)(qj == head ? 2 * qj + 1 : 2 * qj) * a.slot_rows + row) * PS;
 #pragma unroll
                 for (int e = 0; e < C / 2; ++e)
-                    x[j][e] = wj[j] != 0.0f ? __ldcg(reinterpret_cast<const float2 *>(piece(u0 + j0 + j) + lane * C) + e)
+                    x[j][e] = wj[j] != 0.0f ? __ldcg(reinterpret_cast<const float2 *>(src + lane * C) + e)
                                             : make_float2(0.0f, 0.0f);
             }
 #pragma unroll
@@ -645,6 +629,9 @@ __device__ __forceinline__ void dense_join_row(const DenseArgs &a, const DenseCh
                     acc[2 * e + 1] += wj[j] * x[j][e].y;
                 }
         }
+        if (ends)
+            break;
+        q0 += 32;
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll

@@ -30,7 +30,6 @@ constexpr int kOneStages = (WIDE ? 128 : 160) * 1024 / kTileBytes<D>;
 struct OneShared {
     DenseRing<kOneMaxStages> ring;
     uint64_t joined, join_free;
-    int64_t s_warp[kOneThreads / 32];
 };
 
 // WIDE: more than 8 heads.
@@ -279,9 +278,9 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
             before = __shfl_sync(0xffffffffu, before, 0);
             if (before + (uint32_t)(kt1 - kt0) == (uint32_t)tiles) {
                 __threadfence();
-                const DenseChain ch = dense_chain(a, (int)blockIdx.x, kt0 == 0, (int)gridDim.x, lane);
+#pragma unroll 1
                 for (int row = warp; row < a.G; row += kOneWarps)
-                    dense_join_row<D>(a, ch, row, q_row * a.Hq + g * a.G + row, lane);
+                    dense_join_row<D>(a, b, g, 0, counter, (int)gridDim.x, row, q_row * a.Hq + g * a.G + row, lane);
                 if (lane == 0)
                     *count = 0u;                     // as the next call finds it
             }
@@ -312,7 +311,7 @@ dense_one(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
         tma_prefetch_desc(lane ? &vmap : &kmap);
     pdl_wait();
     pdl_launch_dependents();
-    dense_line(a, dense_tables(ring), sh.s_warp);                 // ends with a barrier
+    __syncthreads();
     if (warp == kOneWarps) {
         const QueryLoad<D> none = {};
         load_items<D, kOneStages<D, WIDE>, false>(a, sh.ring, ring, &kmap, &vmap, box, lane, none);

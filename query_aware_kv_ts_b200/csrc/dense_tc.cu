@@ -40,7 +40,6 @@ struct TcShared {
     uint64_t done;
     int32_t bad[kItemSlots];                 // the item's masked tiles held infinities or NaN in V
     uint32_t tmem;
-    int64_t s_warp[kTcThreads / 32];
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], B stored with its N index contiguous.
@@ -629,7 +628,7 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
     pdl_wait();
     pdl_launch_dependents();
     tmem_fence_before();
-    dense_line(a, dense_tables(ring), sh.s_warp);                 // ends with a barrier
+    __syncthreads();
     tmem_fence_after();
 
     if (warp < kSoftmaxWarps) {

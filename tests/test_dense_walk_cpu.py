@@ -15,13 +15,13 @@ HARNESS = os.path.join(ROOT, "tests", "dense_walk_emu.cpp")
 
 
 def walk_source(src: str) -> str:
-    """From the tile's constant to the end of the walk, without the block-wide
-    prefix sum and the warp-wide search (the harness has its own)."""
+    """From the tile's constant to the end of the walk, without the warp-wide
+    search for the next sequence (the harness has its own)."""
     start = src.index("constexpr int kDenseTile")
-    line = src.index("// Fills the tables, one round trip")
+    search = src.index("// The first sequence from b on that has items")
     place = src.index("// A place on the line")
-    end = src.index("// The K / V row of token i < n")
-    return src[start:line] + src[place:end]
+    end = src.index("// The block's part, found by one warp")
+    return src[start:search] + src[place:end]
 
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="no host C++ compiler")
