@@ -444,19 +444,22 @@ ts_status_t make_dense_plan(const ts_kv_t *kv, const int64_t *q_off, DensePlan *
     return TS_OK;
 }
 
-ts_status_t encode_map3(CUtensorMap *map, const void *base, int64_t channels, int64_t dim1, int64_t dim2,
-                        int64_t stride1, int64_t stride2, int box1, int box2)
+ts_status_t encode_tiles(CUtensorMap *map, const void *base, int64_t channels, const TmaDim *dims, int n)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr) {
         set_error("cuTensorMapEncodeTiled is not available from the driver");
         return TS_ERR_CUDA;
     }
-    cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)dim1, (cuuint64_t)dim2};
-    cuuint64_t strides[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride2 * 2};
-    cuuint32_t boxes[3] = {64u, (cuuint32_t)box1, (cuuint32_t)box2}, step[3] = {1u, 1u, 1u};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxes,
-                           step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    cuuint64_t sizes[5] = {(cuuint64_t)channels}, strides[4] = {};
+    cuuint32_t boxes[5] = {64u}, step[5] = {1u, 1u, 1u, 1u, 1u};
+    for (int i = 0; i < n; ++i) {
+        sizes[i + 1] = (cuuint64_t)dims[i].size;
+        strides[i] = (cuuint64_t)dims[i].stride * 2;
+        boxes[i + 1] = (cuuint32_t)dims[i].box;
+    }
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)(n + 1), const_cast<void *>(base), sizes,
+                           strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_error("cuTensorMapEncodeTiled failed (%d)", (int)r);

@@ -40,9 +40,9 @@ dense_merge(const DenseArgs a, int blocks)
 }  // namespace
 
 cudaError_t launch_dense_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                            const DenseArgs &a, int D, int box, int grid, cudaStream_t st);
-cudaError_t launch_dense_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int D, int box,
-                             int grid, cudaStream_t st);
+                            const DenseArgs &a, int D, int grid, cudaStream_t st);
+cudaError_t launch_dense_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int D, int grid,
+                             cudaStream_t st);
 
 void plan_dense(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp)
 {
@@ -69,10 +69,12 @@ void plan_dense(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp)
         }
         items *= p.Hkv;
         tiles *= p.Hkv;
-        // Up to 4 tiles an item is not worth cutting: its pieces' start and
-        // their join cost more than they save.
-        w.split = most > 4;
-        const int64_t parts = w.split ? (tiles + 2) / 3 : items;
+        // One query token: what a block reads, it reads at some 27 bytes a
+        // clock, so a tile to a block where there are few.  Several: up to 4
+        // tiles an item is not worth cutting, its pieces' start and their join
+        // cost more than they save, and pieces have 3 tiles or more.
+        w.split = one ? most > 1 : most > 4;
+        const int64_t parts = !w.split ? items : (one ? tiles : (tiles + 2) / 3);
         w.grid = (int)(parts < p.sms ? (parts > 1 ? parts : items > 0) : p.sms);
         w.slot_rows = one ? 16 : 2 * kStreamRows;
         w.off_pieces = o;
@@ -111,20 +113,31 @@ ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, 
     a.page_shift = p.page_shift;
     a.pool_pages = kv->pool_pages;
 
-    // K and V in boxes of one kv head's 64 channels x up to 128 tokens (a
-    // page, where pages are shorter); Q in boxes of one kv head's query heads
-    // x the tokens of a stream.  A cache without a row is never read from:
-    // its map covers a query row instead, and every token is masked.
-    const int box = p.paged && (1 << p.page_shift) < kDenseTile ? 1 << p.page_shift : kDenseTile;
-    const bool none = p.kv_rows < 1;
+    // K and V boxes: 64 channels x 128 tokens of one kv head; of a paged cache
+    // the rows of a page (128 tokens of it at most), with head_dim 128 as
+    // {64 channels, 8 tokens, both halves of the channels, groups of 8 tokens}.
+    // Q boxes: one kv head's query heads x the tokens of a stream.  A cache
+    // without a row is never read from: its maps cover query rows instead, and
+    // every token is masked.
+    a.box_shift = p.paged && p.page_shift < 7 ? p.page_shift : 7;
+    const int box = 1 << a.box_shift;
+    const bool none = p.kv_rows < 1, pages = p.paged && p.D == 128;
+    a.group_stride = pages ? 2048 : 1024;
+    a.half_stride = pages ? 1024 : kDenseTile * 128;
+    const int64_t rows = none ? 1 : p.kv_rows, st_tok = none ? q_stride_tok : kv->stride_tok,
+                  st_head = none ? p.D : kv->stride_head;
+    const TmaDim by_page[4] = {{8, st_tok, 8}, {2, 64, 2}, {rows / 8, 8 * st_tok, box / 8}, {p.Hkv, st_head, 1}};
+    const TmaDim by_tile[2] = {{rows, st_tok, box}, {p.Hkv, st_head, 1}};
+    const TmaDim by_query[2] = {{p.Hq, p.D, p.G}, {dp.rows, q_stride_tok, kStreamRows / p.G}};
     CUtensorMap kmap, vmap, qmap;
-    ts_status_t s = encode_map3(&kmap, none ? q : kv->k, p.D, none ? 1 : p.kv_rows, p.Hkv,
-                                none ? q_stride_tok : kv->stride_tok, none ? p.D : kv->stride_head, box, 1);
-    if (s == TS_OK)
-        s = encode_map3(&vmap, none ? q : kv->v, p.D, none ? 1 : p.kv_rows, p.Hkv,
-                        none ? q_stride_tok : kv->stride_tok, none ? p.D : kv->stride_head, box, 1);
+    ts_status_t s = TS_OK;
+    for (int kv_ = 0; kv_ < 2 && s == TS_OK; ++kv_) {
+        const void *base = none ? q : (kv_ ? kv->v : kv->k);
+        s = pages ? encode_tiles(kv_ ? &vmap : &kmap, base, 64, by_page, 4)
+                  : encode_tiles(kv_ ? &vmap : &kmap, base, p.D, by_tile, 2);
+    }
     if (s == TS_OK && dp.launch[0].grid > 0)
-        s = encode_map3(&qmap, q, p.D, p.Hq, dp.rows, p.D, q_stride_tok, p.G, kStreamRows / p.G);
+        s = encode_tiles(&qmap, q, p.D, by_query, 2);
     if (s != TS_OK)
         return s;
     for (int one = 1; one >= 0; --one) {
@@ -139,8 +152,8 @@ ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, 
         a.counts = reinterpret_cast<uint32_t *>(ws + dp.off_counts);
         a.pieces = reinterpret_cast<DensePiece *>(ws + w.off_pieces);
         a.part = reinterpret_cast<float *>(ws + w.off_part);
-        cudaError_t e = one ? launch_dense_one(kmap, vmap, a, p.D, box, w.grid, st)
-                            : launch_dense_tc(qmap, kmap, vmap, a, p.D, box, w.grid, st);
+        cudaError_t e = one ? launch_dense_one(kmap, vmap, a, p.D, w.grid, st)
+                            : launch_dense_tc(qmap, kmap, vmap, a, p.D, w.grid, st);
         if (e == cudaSuccess && !one && w.split && w.grid > 1) {
             const dim3 grid(w.grid - 1, 8);
             e = p.D == 128 ? launch_ex(dense_merge<128>, grid, dim3(kMergeWarps * 32), 0, st, 1, a, w.grid)

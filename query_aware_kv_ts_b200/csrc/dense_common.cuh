@@ -55,6 +55,12 @@ struct DenseArgs {
     const int32_t *page_table;
     int pt_stride, page_shift;
     int64_t pool_pages;
+    // K and V tiles in shared memory: rows of 64 channels (128 bytes, 128-byte
+    // swizzle), 8 tokens together; bytes from 8 tokens to the next 8, and from
+    // the first 64 channels to the others.  A paged cache's boxes hold whole
+    // rows of some tokens, a packed one's 64 channels of all 128.
+    int group_stride, half_stride;
+    int box_shift;        // log2 of the tokens of one box
 };
 
 struct DenseItem {
@@ -65,7 +71,9 @@ struct DenseItem {
     int32_t slot;              // -1: the whole item; else its piece's place in the partial results
     int64_t q_row;             // its first query row
     int64_t off, n, first_pos; // the sequence's first row and length; position of its first query token
-    int32_t counter;           // for the shared items, a number below gridDim.x of each one's own
+    int64_t line;              // the sequence's beginning on the line, and its query tokens
+    int32_t f;
+    int32_t counter;           // dense_counter, of a shared item
 };
 
 // Cost of an item beside its tokens, in tokens: measured start and end of an item.
@@ -73,7 +81,8 @@ constexpr int kItemCost = 192;
 
 __device__ __forceinline__ int64_t seq_items(const DenseArgs &a, int64_t f)
 {
-    return (a.single ? f == 1 : f > 1) ? (f + a.TT - 1) / a.TT : 0;
+    // (f stays below 2^25: a 32-bit division)
+    return a.single ? f == 1 : (f > 1 ? ((uint32_t)f + (uint32_t)a.TT - 1u) / (uint32_t)a.TT : 0u);
 }
 // Length of the first t items of one kv head of a sequence on the line:
 // item s counts base + (s + 1) TT + kItemCost.
@@ -268,19 +277,8 @@ struct DenseWalk {
         it.off = at.off;
         it.q_row = at.q0 + (int64_t)at.t * a.TT;
         it.n = at.n;
-        it.counter = 0;
-        if (it.slot >= 0) {
-            // the part in which the item begins: an item that a part's end
-            // cuts is the last to begin in its part
-            const int64_t x =
-                at.line + at.g * dense_head_cost(a, at) + items_cost(a, at.n > at.f ? at.n - at.f : 0, at.t);
-            int c = (int)((double)x * (double)gridDim.x / (double)total);
-            while (dense_part(a, total, c) > x)
-                --c;
-            while (dense_part(a, total, c + 1) <= x)
-                ++c;
-            it.counter = c;
-        }
+        it.line = at.line;
+        it.f = (int32_t)at.f;
         it.first_pos = at.n - at.f + (int64_t)at.t * a.TT;
         if (last)
             at.cut = end.cut;                                // next() ends here
@@ -289,6 +287,21 @@ struct DenseWalk {
         return true;
     }
 };
+
+// A number below gridDim.x of each shared item's own, the same for all its
+// pieces: the part in which it begins (an item that a part's end cuts is the
+// last to begin in its part).
+__device__ __forceinline__ int32_t dense_counter(const DenseArgs &a, const DenseItem &it, int64_t total)
+{
+    const int64_t base = it.n > it.f ? it.n - it.f : 0;
+    const int64_t x = it.line + it.g * items_cost(a, base, seq_items(a, it.f)) + items_cost(a, base, it.t);
+    int c = min((int)((float)x * (float)gridDim.x / (float)total), (int)gridDim.x - 1);
+    while (dense_part(a, total, c) > x)
+        --c;
+    while (dense_part(a, total, c + 1) <= x)
+        ++c;
+    return c;
+}
 
 // The block's part, found by one warp: the tables (in shared memory, where the
 // tiles will be) after one round trip to the offsets, 32 sequences at a time,
@@ -410,15 +423,38 @@ struct QueryLoad {
     int32_t *bad;                            // per item slot, cleared when an item begins
 };
 
-__device__ __forceinline__ void tma_load_tile(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
+__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
                                               int32_t z)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+// Whole rows of a page's tokens: {64 channels, 8 tokens, 2 halves, groups of 8, 1 head}.
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t group,
+                                              int32_t head)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(group), "r"(head)
+        : "memory");
+}
+
+// One lane of the warp, the same each time.  What one lane issues from code
+// that the whole warp walks keeps its operands in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -454,20 +490,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32
 }
 
 // The loading warp: walks the block's items, publishes each, and streams its
-// K and V tiles (K and V of a tile in turn; 64-channel halves of 128-byte
-// rows, 128-byte swizzle) into the ring, and with QL its queries.  A tile is
-// one box {64 channels, 128 tokens, 1 head} per half, or in a paged cache with
-// shorter pages one box per page and half, each issued by its own lane.  An
-// item with b < 0 ends the line.
+// K and V tiles (K and V of a tile in turn) into the ring, and with QL its
+// queries.  A packed cache's tile is a box of all 128 tokens per 64 channels;
+// a paged one's a box per page, or per 128 tokens of one (a box costs its
+// issue, so with 16-token pages one box for both halves of the channels
+// counts).  An item with b < 0 ends the line.
 template <int D, int NS, bool QL, int MAXNS>
-__device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> &r, uint8_t *ring, const CUtensorMap *kmap, const CUtensorMap *vmap, int box,
-                                           int lane, const QueryLoad<D> &q)
+__device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> &r, uint8_t *ring,
+                                           const CUtensorMap *kmap, const CUtensorMap *vmap, int lane,
+                                           const QueryLoad<D> &q)
 {
     const int T = kStreamRows / a.G;
-    const int npp = kDenseTile / box;                // boxes along a tile's tokens
-    const int p = lane % npp, half = lane / npp;     // this lane's box: page p of the tile, 64 channels
-    const bool mine = lane < npp * (D / 64);
-    const int64_t oob = a.pool_pages << a.page_shift;   // past the pool: reads zeros
+    const int log_pages = 7 - a.box_shift;           // boxes along a tile's 128 tokens
+    const int ahead = 31 >> log_pages;               // tiles, less one, whose pages one round trip finds
+    const int32_t oob = (int32_t)(a.pool_pages << a.page_shift);   // past the pool: reads zeros
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(r.full);
     DenseWalk w;
     dense_begin(a, ring, lane, w);
     fence_proxy_async_smem();                        // the tables are read: tiles may go over them
@@ -499,47 +536,77 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
                 ok = false;
                 break;
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 const int streams = it.tokens > T ? 2 : 1;
                 mbar_arrive_expect_tx(q.full, (uint32_t)(streams * T * a.G * D * 2));
                 for (int s = 0; s < streams; ++s)
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
-                        tma_load_tile(q.sq + (s * (D / 64) + x) * (kStreamRows * 128), q.map, q.full, x * 64,
-                                      it.g * a.G, (int32_t)(it.q_row + s * T));
+                        tma_load_tile(smem_u32(q.sq) + (s * (D / 64) + x) * (kStreamRows * 128), q.map,
+                                      smem_u32(q.full), x * 64, it.g * a.G, (int32_t)(it.q_row + s * T));
             }
+            __syncwarp();
         }
-        int32_t row = 0;
-        for (int kt = it.kt0; kt < it.kt1 && ok; ++kt) {
-            const int ahead = (kt - it.kt0) % (32 / npp);
-            int32_t y;
-            if (a.page_table == nullptr) {
-                y = (int32_t)(it.off + (int64_t)kt * kDenseTile);
-            } else {
-                if (ahead == 0) {
-                    // one round trip to the block table finds the pages of the
-                    // next 32 / npp tiles, one page a lane
-                    const int64_t i = (int64_t)(kt + lane / npp) * kDenseTile + (int64_t)p * box;
-                    const int64_t found = i < it.n ? dense_row(a, it.b, it.off, i) : -1;
-                    row = (int32_t)(found < 0 ? oob : found);
+        const int kt0 = uniform(it.kt0), kt1 = uniform(it.kt1), g = uniform(it.g);
+        int32_t row = uniform((int32_t)(it.off + (int64_t)kt0 * kDenseTile));
+        for (int kt = kt0; kt < kt1 && ok; ++kt) {
+            const int done = (kt - kt0) & ahead;
+            if (a.page_table != nullptr && done == 0) {
+                // one round trip to the block table finds the pages of the
+                // next tiles, one page a lane
+                const int64_t i = ((int64_t)kt << 7) + ((int64_t)lane << a.box_shift);
+                row = oob;
+                if (i < it.n) {
+                    const int32_t pg = __ldcg(a.page_table + (int64_t)it.b * a.pt_stride + (i >> a.page_shift));
+                    if (pg >= 0 && pg < a.pool_pages)
+                        row = (pg << a.page_shift) + (int32_t)(i & ((1 << a.page_shift) - 1));
                 }
-                y = __shfl_sync(0xffffffffu, row, ahead * npp + p);
             }
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
+                // (wanted at the item's end only; written before the arrival
+                // for its first V tile, it is there by then)
+                if (kv == 1 && kt == kt0 && it.slot >= 0 && !QL) {
+                    const int32_t c = dense_counter(a, it, w.total);
+                    if (elect_one())
+                        r.item[slot].counter = c;
+                    __syncwarp();
+                }
                 const int st = n % NS;
                 if (n >= (uint32_t)NS && !warp_wait(&r.empty[st], ((n / NS) - 1) & 1, a.ctrl, lane)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0)
+                const CUtensorMap *map = kv ? vmap : kmap;
+                const uint32_t dst = ring0 + st * kTileBytes<D>, bar = full0 + st * 8;
+                if (elect_one())
                     mbar_arrive_expect_tx(&r.full[st], (uint32_t)kTileBytes<D>);
                 __syncwarp();
-                if (mine)
-                    tma_load_tile(ring + st * kTileBytes<D> + half * (kDenseTile * 128) + p * box * 128,
-                                  kv ? vmap : kmap, &r.full[st], half * 64, y, it.g);
+                if (a.page_table == nullptr) {
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_tile(dst + x * (kDenseTile * 128), map, bar, x * 64, row, g);
+                    }
+                    __syncwarp();
+                } else {
+#pragma unroll 4
+                    for (int p = 0; p < 1 << log_pages; ++p) {
+                        const int32_t y = __shfl_sync(0xffffffffu, row, (done << log_pages) + p);
+                        if (elect_one()) {
+                            const uint32_t to = dst + ((p * D * 2) << a.box_shift);
+                            if (D == 128)
+                                tma_load_page(to, map, bar, y >> 3, g);
+                            else
+                                tma_load_tile(to, map, bar, 0, y, g);
+                        }
+                        __syncwarp();
+                    }
+                }
                 ++n;
             }
+            if (a.page_table == nullptr)
+                row += kDenseTile;
         }
     }
     // a wait gave up: no more loads are issued; wait (bounded) for those in

@@ -46,6 +46,8 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
     // channels), V's are transposed on the way
     const int k_tok = warp * 16 + (lane & 7) + (lane >> 4) * 8, k_chunk = (lane >> 3) & 1;
     const int v_tok = warp * 16 + (lane & 15), v_chunk = lane >> 4;
+    const int k_row = (k_tok >> 3) * a.group_stride + (k_tok & 7) * 128;
+    const int v_row = (v_tok >> 3) * a.group_stride + (v_tok & 7) * 128;
     uint32_t n = 0;
     for (uint32_t k = 0;; ++k) {
         const int slot = k % kItemSlots;
@@ -55,7 +57,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
         if (b < 0)
             return;
         const int g = sh.ring.item[slot].g, kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
-        const int part_slot = sh.ring.item[slot].slot, counter = sh.ring.item[slot].counter;
+        const int part_slot = sh.ring.item[slot].slot;
         const int tiles = sh.ring.item[slot].tiles;
         const int64_t q_row = sh.ring.item[slot].q_row, len = sh.ring.item[slot].n;
         uint32_t qa[D / 16][4];
@@ -70,9 +72,6 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                     qa[ks][e] = __ldcg(reinterpret_cast<const uint32_t *>(q + (int64_t)row * D + ks * 16 + c0 +
                                                                           (e >> 1) * 8));
             }
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sh.ring.item_empty[slot]);
         // weighted sums: rows r0 and r0 + 8 (up to 8 heads, the remainders')
         float o[D / 8][4];
 #pragma unroll
@@ -91,12 +90,12 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 s[0][e] = s[1][e] = 0.0f;
-            const uint32_t kb = ring + sk * kTileBytes<D> + k_tok * 128;
+            const uint32_t kb = ring + sk * kTileBytes<D> + k_row;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t b0, b1, b2, b3;
                 ldmatrix_x4(b0, b1, b2, b3,
-                            kb + (ks >> 2) * (kDenseTile * 128) + (((((ks & 3) * 2 + k_chunk) ^ (k_tok & 7))) << 4));
+                            kb + (ks >> 2) * a.half_stride + (((((ks & 3) * 2 + k_chunk) ^ (k_tok & 7))) << 4));
                 mma_16816(s[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
                 mma_16816(s[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
             }
@@ -162,7 +161,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
             // ---- O += P V ----
             if (!warp_wait(&sh.ring.full[sv], ((n + 1) / NS) & 1, a.ctrl, lane))
                 return;
-            const uint32_t vb = ring + sv * kTileBytes<D> + v_tok * 128;
+            const uint32_t vb = ring + sv * kTileBytes<D> + v_row;
             // rows behind the sequence's end hold anything: no weight of zero
             // takes a NaN away, so they go in as zeros
             uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
@@ -174,7 +173,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
             for (int i = 0; i < D / 8; i += 2) {
                 uint32_t b0, b1, b2, b3;
                 ldmatrix_x4_trans(b0, b1, b2, b3,
-                                  vb + (i >> 3) * (kDenseTile * 128) + ((((i & 7) + v_chunk) ^ (v_tok & 7)) << 4));
+                                  vb + (i >> 3) * a.half_stride + ((((i & 7) + v_chunk) ^ (v_tok & 7)) << 4));
                 b0 &= keep0;
                 b1 &= keep1;
                 b2 &= keep0;
@@ -193,6 +192,10 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
             if (lane == 0)
                 mbar_arrive(&sh.ring.empty[sv]);
         }
+        const int counter = sh.ring.item[slot].counter;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.ring.item_empty[slot]);
         // ---- the eight warps' sums joined, in a fixed order ----
         if (k > 0 && !warp_wait(&sh.join_free, (k - 1) & 1, a.ctrl, lane))
             return;
@@ -294,7 +297,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kOneThreads, 1)
 dense_one(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-          const __grid_constant__ DenseArgs a, int box)
+          const __grid_constant__ DenseArgs a)
 {
     extern __shared__ uint8_t dyn_smem[];
     __shared__ OneShared sh;
@@ -314,33 +317,32 @@ dense_one(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUte
     __syncthreads();
     if (warp == kOneWarps) {
         const QueryLoad<D> none = {};
-        load_items<D, kOneStages<D, WIDE>, false>(a, sh.ring, ring, &kmap, &vmap, box, lane, none);
+        load_items<D, kOneStages<D, WIDE>, false>(a, sh.ring, ring, &kmap, &vmap, lane, none);
     } else {
         attend_items<D, WIDE>(a, sh, smem_u32(ring), join, warp, lane);
     }
 }
 
 template <int D, bool WIDE>
-cudaError_t launch_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int box, int grid,
-                       cudaStream_t st)
+cudaError_t launch_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int grid, cudaStream_t st)
 {
     const size_t smem = 1024 + (size_t)kOneStages<D, WIDE> * kTileBytes<D> + kJoinBytes<D, WIDE>;
     const cudaError_t e = ensure_dyn_smem((const void *)dense_one<D, WIDE>, (int)smem);
     if (e != cudaSuccess)
         return e;
-    return launch_ex(dense_one<D, WIDE>, dim3(grid), dim3(kOneThreads), smem, st, 1, kmap, vmap, a, box);
+    return launch_ex(dense_one<D, WIDE>, dim3(grid), dim3(kOneThreads), smem, st, 1, kmap, vmap, a);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int D, int box,
-                             int grid, cudaStream_t st)
+cudaError_t launch_dense_one(const CUtensorMap &kmap, const CUtensorMap &vmap, const DenseArgs &a, int D, int grid,
+                             cudaStream_t st)
 {
     if (D == 128)
-        return a.G > 8 ? launch_one<128, true>(kmap, vmap, a, box, grid, st)
-                       : launch_one<128, false>(kmap, vmap, a, box, grid, st);
-    return a.G > 8 ? launch_one<64, true>(kmap, vmap, a, box, grid, st)
-                   : launch_one<64, false>(kmap, vmap, a, box, grid, st);
+        return a.G > 8 ? launch_one<128, true>(kmap, vmap, a, grid, st)
+                       : launch_one<128, false>(kmap, vmap, a, grid, st);
+    return a.G > 8 ? launch_one<64, true>(kmap, vmap, a, grid, st)
+                   : launch_one<64, false>(kmap, vmap, a, grid, st);
 }
 
 }  // namespace ts

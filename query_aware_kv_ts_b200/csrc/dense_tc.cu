@@ -55,12 +55,19 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
 
 // Shared-memory descriptor of an operand whose M / N index is contiguous:
 // 64-channel blocks of 128-byte rows (one row a token), 128-byte swizzle.
-// 8 tokens are 1024 bytes apart (stride), 64-channel blocks block_bytes
+// 8 tokens are group bytes apart (stride), 64-channel blocks half bytes
 // (leading dimension).
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t smem_addr, uint32_t block_bytes)
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t smem_addr, uint32_t group, uint32_t half)
 {
-    return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)(block_bytes >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+    return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)(half >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// The same for K, whose channels are the sum's index: 64 channels a row, 8
+// tokens group bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_sw128_k(uint32_t smem_addr, uint32_t group)
+{
+    return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)1 << 16) | ((uint64_t)(group >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v)
@@ -398,17 +405,6 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
 // depend on is the same in every lane and stays in uniform registers, where
 // the instruction wants it (a walk of one lane spent 100 cycles an MMA on
 // bringing its operands there, more than the 64 that the product takes).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok));
-    return ok != 0;
-}
-
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
 template <int D, int NS>
 __device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh, uint32_t sq, uint32_t ring, int lane)
 {
@@ -416,25 +412,27 @@ __device__ __forceinline__ void issue_products(const DenseArgs &a, TcShared &sh,
     constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | (1u << 16);   // B's N index is contiguous
     const int T = kStreamRows / a.G;
     const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
+    const uint32_t group = a.group_stride, half = a.half_stride;
     uint32_t n = 0;                                  // tiles consumed
     uint32_t p_phase[2] = {0, 0}, clean = 0;
     // one lane: S of stream s = Q K^T with K in stage st
     auto scores = [&](int s, int st) {
         const uint64_t q = umma_desc_sw128(sq + s * (kStreamRows * D * 2));
-        const uint64_t k = umma_desc_sw128(ring + st * kTileBytes<D>);
+        const uint64_t k = umma_desc_sw128_k(ring + st * kTileBytes<D>, group);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t off = (uint64_t)(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
-            umma_bf16(tmem + s * 128, q + off, k + off, idesc_s, ks > 0);
+            const uint32_t in = (ks & 3) * 2;        // 32 bytes a step inside the 128-byte row
+            umma_bf16(tmem + s * 128, q + (uint64_t)((ks >> 2) * (128 * 128 >> 4) + in),
+                      k + (uint64_t)((ks >> 2) * (half >> 4) + in), idesc_s, ks > 0);
         }
         umma_commit(&sh.s_full[s]);
     };
     // one lane: O of stream s (+)= P V with V in stage st
     auto values = [&](int s, int st, bool more) {
-        const uint64_t v = umma_desc_sw128_mn(ring + st * kTileBytes<D>, kDenseTile * 128);
+        const uint64_t v = umma_desc_sw128_mn(ring + st * kTileBytes<D>, group, half);
 #pragma unroll
         for (int ks = 0; ks < kDenseTile / 16; ++ks)
-            umma_bf16_ts(tmem + kTmemO + s * D, tmem + s * 128 + ks * 8, v + (uint64_t)(ks * 2048 >> 4), idesc_o,
+            umma_bf16_ts(tmem + kTmemO + s * D, tmem + s * 128 + ks * 8, v + (uint64_t)(ks * (2 * group >> 4)), idesc_o,
                          more || ks > 0);
     };
     for (uint32_t k = 0;; ++k) {
@@ -556,23 +554,26 @@ __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, u
                     mbar_arrive(&sh.ring.empty[st]);
                 continue;
             }
-            uint4 *tile = reinterpret_cast<uint4 *>(ring + st * kTileBytes<D>);
             // tokens seen by all rows, by some, by none (of the tile's 128)
             const int64_t t0 = (int64_t)kt * kDenseTile;
             const int all = (int)max(min(first + 1 - t0, (int64_t)kDenseTile), (int64_t)0);
             const int some = (int)max(min(last + 1 - t0, (int64_t)kDenseTile), (int64_t)all);
             bool bad = false;
             for (int half = 0; half < D / 64; ++half) {
-                uint4 *rows = tile + half * (kDenseTile * 8);   // 8 pieces of 16 bytes a token
+                uint8_t *rows = ring + st * kTileBytes<D> + half * a.half_stride + (lane & 7) * 16;
+                // 8 pieces of 16 bytes a token, 4 tokens at a time
+                auto piece = [&](int t) {
+                    return reinterpret_cast<uint4 *>(rows + (t >> 3) * a.group_stride + (t & 7) * 128);
+                };
 #pragma unroll 4
-                for (int i = some * 8 + lane; i < kDenseTile * 8; i += 32)
-                    rows[i] = make_uint4(0u, 0u, 0u, 0u);
-                for (int i = all * 8 + lane; i < some * 8; i += 32) {
-                    const uint4 x = rows[i];
+                for (int t = some + (lane >> 3); t < kDenseTile; t += 4)
+                    *piece(t) = make_uint4(0u, 0u, 0u, 0u);
+                for (int t = all + (lane >> 3); t < some; t += 4) {
+                    const uint4 x = *piece(t);
                     const uint4 w = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
                                                finite_or_zero(x.w));
                     if (w.x != x.x || w.y != x.y || w.z != x.z || w.w != x.w) {
-                        rows[i] = w;
+                        *piece(t) = w;
                         bad = true;
                     }
                 }
@@ -595,7 +596,7 @@ __device__ __forceinline__ void guard_values(const DenseArgs &a, TcShared &sh, u
 template <int D, int NS>
 __global__ void __launch_bounds__(kTcThreads, 1)
 dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DenseArgs a, int box)
+         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DenseArgs a)
 {
     // all of it dynamic, without padding: five 32 KB tiles and Q leave 3 KB
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
@@ -638,7 +639,7 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAuxRegs));
         if (warp == kLoadWarp) {
             const QueryLoad<D> q = {&qmap, sq, &sh.q_full, &sh.q_empty, sh.bad};
-            load_items<D, NS, true>(a, sh.ring, ring, &kmap, &vmap, box, lane, q);
+            load_items<D, NS, true>(a, sh.ring, ring, &kmap, &vmap, lane, q);
         } else if (warp == kMmaWarp) {
             issue_products<D, NS>(a, sh, smem_u32(sq), smem_u32(ring), lane);
             // every MMA issued has completed before TMEM is released
@@ -662,21 +663,21 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
 
 template <int D, int NS>
 static cudaError_t launch_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                             const DenseArgs &a, int box, int grid, cudaStream_t st)
+                             const DenseArgs &a, int grid, cudaStream_t st)
 {
     constexpr size_t smem = (size_t)2 * kStreamRows * D * 2 + (size_t)NS * kTileBytes<D> + sizeof(TcShared);
     static_assert(smem <= 227 * 1024 && kDenseTableBytes <= NS * kTileBytes<D>, "shared memory");
     const cudaError_t e = ensure_dyn_smem((const void *)dense_tc<D, NS>, (int)smem);
     if (e != cudaSuccess)
         return e;
-    return launch_ex(dense_tc<D, NS>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a, box);
+    return launch_ex(dense_tc<D, NS>, dim3(grid), dim3(kTcThreads), smem, st, 1, qmap, kmap, vmap, a);
 }
 
 cudaError_t launch_dense_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                            const DenseArgs &a, int D, int box, int grid, cudaStream_t st)
+                            const DenseArgs &a, int D, int grid, cudaStream_t st)
 {
-    return D == 128 ? launch_tc<128, 5>(qmap, kmap, vmap, a, box, grid, st)
-                    : launch_tc<64, 8>(qmap, kmap, vmap, a, box, grid, st);
+    return D == 128 ? launch_tc<128, 5>(qmap, kmap, vmap, a, grid, st)
+                    : launch_tc<64, 8>(qmap, kmap, vmap, a, grid, st);
 }
 
 }  // namespace ts

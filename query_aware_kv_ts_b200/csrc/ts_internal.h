@@ -245,10 +245,14 @@ void plan_dense(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp);   // fi
 ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, int64_t q_stride_tok,
                          const int64_t *q_off, void *out, float *lse, uint8_t *ws, cudaStream_t st);
 
-// A bf16 tensor [dim2][dim1][channels] (strides in elements) in TMA boxes
-// {64 channels, box1, box2} with the 128-byte swizzle; zeros outside it.
-ts_status_t encode_map3(CUtensorMap *map, const void *base, int64_t channels, int64_t dim1, int64_t dim2,
-                        int64_t stride1, int64_t stride2, int box1, int box2);
+// A bf16 tensor of `channels` contiguous channels and 2 to 4 further dimensions
+// (innermost first), in TMA boxes of 64 channels and each dimension's box with
+// the 128-byte swizzle; zeros outside it.
+struct TmaDim {
+    int64_t size, stride;    // stride in elements
+    int box;
+};
+ts_status_t encode_tiles(CUtensorMap *map, const void *base, int64_t channels, const TmaDim *dims, int n);
 
 // Token-axis split of one sequence (split.cu): the joins' arithmetic.
 cudaError_t launch_merge_normalisers(const double *L_parts, int parts, int64_t count, double *L_out,

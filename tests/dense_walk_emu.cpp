@@ -93,7 +93,8 @@ int main()
                 ok &= it.kt0 < it.kt1 && it.off == so[it.b] && it.q_row == qo[it.b] + (int64_t)it.t * a.TT;
                 ok &= it.n == so[it.b + 1] - so[it.b];
                 ok &= it.first_pos == it.n - (qo[it.b + 1] - qo[it.b]) + (int64_t)it.t * a.TT;
-                got[Key(it.b, it.g, it.t)].push_back({it.kt0, it.kt1, it.slot, it.tiles, it.tokens, it.counter});
+                got[Key(it.b, it.g, it.t)].push_back({it.kt0, it.kt1, it.slot, it.tiles, it.tokens,
+                                                          it.slot >= 0 ? dense_counter(a, it, w.total) : 0});
             }
         }
         size_t items = 0;
