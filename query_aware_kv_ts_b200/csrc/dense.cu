@@ -13,6 +13,10 @@ namespace {
 
 constexpr int kMergeWarps = 8;
 
+// What an item costs beside its tokens, in tokens (half a tile for the last
+// one's rest included).
+constexpr int kOneItemCost = 192, kTcItemCost = 400;
+
 // The shared items of dense_tc: a block of this kernel for each block of that
 // one and group of rows; those whose block begins no shared item return.  One
 // warp a row.  (dense_one's blocks join theirs themselves, a few rows an item;
@@ -147,6 +151,7 @@ ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, 
         a.TT = w.TT;
         a.single = one;
         a.split = w.split;
+        a.item_cost = one ? kOneItemCost : kTcItemCost;
         a.inv_grid = 1.0 / w.grid;
         a.slot_rows = w.slot_rows;
         a.counts = reinterpret_cast<uint32_t *>(ws + dp.off_counts);

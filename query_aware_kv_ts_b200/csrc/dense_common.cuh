@@ -46,6 +46,7 @@ struct DenseArgs {
     int TT;               // query tokens per item
     int single;           // 1: the sequences with one query token, 0: those with more
     int split;            // 0: parts end between items only
+    int item_cost;        // what an item's beginning and end take, in tokens of its tiles
     double inv_grid;      // 1 / blocks
     int slot_rows;        // rows of one partial result
     uint32_t *counts;     // [grid][8], zero between calls: tiles done of the items that blocks share
@@ -76,19 +77,16 @@ struct DenseItem {
     int32_t counter;           // dense_counter, of a shared item
 };
 
-// Cost of an item beside its tokens, in tokens: measured start and end of an item.
-constexpr int kItemCost = 192;
-
 __device__ __forceinline__ int64_t seq_items(const DenseArgs &a, int64_t f)
 {
     // (f stays below 2^25: a 32-bit division)
     return a.single ? f == 1 : (f > 1 ? ((uint32_t)f + (uint32_t)a.TT - 1u) / (uint32_t)a.TT : 0u);
 }
 // Length of the first t items of one kv head of a sequence on the line:
-// item s counts base + (s + 1) TT + kItemCost.
+// item s counts base + (s + 1) TT + a.item_cost.
 __device__ __forceinline__ int64_t items_cost(const DenseArgs &a, int64_t base, int64_t t)
 {
-    return t * (base + kItemCost) + (int64_t)a.TT * (t * (t + 1) / 2);
+    return t * (base + a.item_cost) + (int64_t)a.TT * (t * (t + 1) / 2);
 }
 
 // The first sequence from b on that has items, B if none has.  Whole warp, 32
@@ -208,8 +206,8 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const Den
     rem -= items_cost(a, base, t0);
     dense_item_at(a, p);
     if (a.split) {
-        const int32_t c = rem < kItemCost - kDenseTile / 2 ? 0
-                              : (int32_t)((rem - kItemCost + kDenseTile / 2) / kDenseTile);
+        const int32_t c = rem < a.item_cost - kDenseTile / 2 ? 0
+                              : (int32_t)((rem - a.item_cost + kDenseTile / 2) / kDenseTile);
         p.cut = c < p.tiles ? c : p.tiles;
         if (p.tiles >= 8) {                    // no piece of a single tile
             if (p.cut < 2)
@@ -218,7 +216,7 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const Den
                 p.cut = p.tiles;
         }
     } else {
-        p.cut = 2 * rem < base + (t0 + 1) * a.TT + kItemCost ? 0 : p.tiles;
+        p.cut = 2 * rem < base + (t0 + 1) * a.TT + a.item_cost ? 0 : p.tiles;
     }
     if (p.cut == p.tiles) {                    // the next item's beginning
         p.cut = 0;

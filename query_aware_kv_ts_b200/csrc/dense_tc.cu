@@ -166,39 +166,37 @@ __device__ __forceinline__ void transpose4(uint4 (&w)[4], int lane)
     swap(w[1], w[3], 2);
 }
 
-// The item's end for this thread's row: O / l to the output, or O, m and
-// l to the partial results.  mb: the row's reference in base 2.  Four lanes
+// Where the rows of a lane's quad go, apart from the item: token and head of
+// each in the stream, and its row of the output behind the stream's first.
+struct QuadRows {
+    int32_t token[4], row[4];
+};
+
+// The item's end for this thread's row: O / l to the output, or O, m and l to
+// the partial results.  mb: the row's reference in base 2.  Four lanes
 // exchange 16-byte pieces first, so that a store covers 8 rows of 64 bytes
 // and not 32 of 16.
 template <int D>
 __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &it, bool bad, int stream, int r,
-                                           int lane, uint32_t to, float mb, float l)
+                                           int lane, const QuadRows &rows, uint32_t to, float mb, float l)
 {
-    const int T = kStreamRows / a.G;
-    const int tokens = min(T, it.tokens - stream * T);
-    const bool whole = it.slot < 0;
+    const int T = kStreamRows / a.G, me = lane & 3;
+    const int tokens = min(T, it.tokens - stream * T), slot = it.slot;
+    const bool whole = slot < 0;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int quad = r & ~3, piece = lane & 3;
-    // the rows of this lane's quad: where they go in the output, and (in out-
-    // and part-row order) whether they are rows of the item
-    int64_t base[4];
-    bool live[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int token = (quad + u) / a.G, head = (quad + u) - token * a.G;
-        live[u] = token < tokens;
-        base[u] = whole ? ((it.q_row + stream * T + token) * a.Hq + it.g * a.G + head) * D
-                        : ((int64_t)it.slot * a.slot_rows + stream * kStreamRows + quad + u) * (D + 4);
-    }
+    const int64_t row0 = (it.q_row + stream * T) * a.Hq + it.g * a.G;
+    const int my_token = me < 2 ? (me ? rows.token[1] : rows.token[0]) : (me == 2 ? rows.token[2] : rows.token[3]);
+    const int my_row = me < 2 ? (me ? rows.row[1] : rows.row[0]) : (me == 2 ? rows.row[2] : rows.row[3]);
+    __nv_bfloat16 *out = a.out + row0 * D + me * 8;
+    float *part = a.part + ((int64_t)slot * a.slot_rows + stream * kStreamRows + (r & ~3)) * (D + 4) + me * 4;
 #pragma unroll 1
     for (int x = 0; x < D; x += 32) {
         uint32_t o[32];
         tmem_ld32(to + x, o);
         tmem_wait_ld();
-        const int token = r / a.G;
-        if (bad && token < tokens) {
+        if (bad && my_token < tokens) {
             // infinities and NaN of the masked tiles that this row sees
-            const int64_t pos = it.first_pos + stream * T + token;
+            const int64_t pos = it.first_pos + stream * T + my_token;
             const int64_t t0 = max(it.first_pos + 1, (int64_t)it.kt0 * kDenseTile);
             const int64_t t1 = min(pos + 1, (int64_t)it.kt1 * kDenseTile);
             for (int64_t t = t0; t < t1; ++t) {
@@ -225,8 +223,8 @@ __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &
             transpose4(w, lane);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (live[u])
-                    *reinterpret_cast<uint4 *>(a.out + base[u] + x + piece * 8) = w[u];
+                if (rows.token[u] < tokens)
+                    *reinterpret_cast<uint4 *>(out + rows.row[u] * D + x) = w[u];
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -237,18 +235,17 @@ __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &
                 transpose4(w, lane);
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (live[u])
-                        *reinterpret_cast<uint4 *>(a.part + base[u] + x + h * 16 + piece * 4) = w[u];
+                    if (rows.token[u] < tokens)
+                        *reinterpret_cast<uint4 *>(part + u * (D + 4) + x + h * 16) = w[u];
             }
         }
     }
-    const int token = r / a.G, head = r - token * a.G;
-    if (token < tokens && !whole)
-        *reinterpret_cast<float2 *>(a.part + ((int64_t)it.slot * a.slot_rows + stream * kStreamRows + r) *
-                                                 (D + 4) + D) = make_float2(mb, l);
-    else if (token < tokens && a.lse != nullptr)
-        a.lse[(it.q_row + stream * T + token) * a.Hq + it.g * a.G + head] =
-            l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
+    if (my_token < tokens) {
+        if (!whole)
+            *reinterpret_cast<float2 *>(part + me * D + D) = make_float2(mb, l);   // of row `me` of the quad
+        else if (a.lse != nullptr)
+            a.lse[row0 + my_row] = l == 0.0f ? -INFINITY : (mb + log2f(l)) * kLn2f;
+    }
 }
 
 __device__ __forceinline__ void load_scores(uint32_t ts, bool negative, float (&s)[32])
@@ -292,23 +289,30 @@ __device__ __forceinline__ float tile_weights(uint32_t ts, float m, float c, boo
     return y0 + y1;
 }
 
-// The largest score that the row sees in the tile.
-__device__ __forceinline__ float tile_top(uint32_t ts, bool negative, int limit)
+// The largest score that the row sees among the tile's first `chunks` x 32.
+__device__ __forceinline__ float tile_top(uint32_t ts, bool negative, int limit, int chunks)
 {
     float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int x = 0; x < kDenseTile / 32; ++x) {
+#pragma unroll 1
+    for (int x = 0; x < chunks; ++x, limit -= 32) {
         float s[32];
         load_scores(ts + x * 32, negative, s);
+        if (limit >= 32) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            top[e & 1] = fmaxf(top[e & 1], x * 32 + e < limit ? s[e] : -INFINITY);
+            for (int e = 0; e < 32; ++e)
+                top[e & 1] = fmaxf(top[e & 1], s[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                top[e & 1] = fmaxf(top[e & 1], e < limit ? s[e] : -INFINITY);
+        }
+        __syncwarp();
     }
     return fmaxf(top[0], top[1]);
 }
 
 // ---- the softmax of one stream: 128 threads, one row each -------------------
-// A row's reference m is the maximum of its first tile.  A later tile's
+// A row's reference m is the largest of the first scores that it sees.  A tile's
 // weights are taken with m as it stands: they may grow above 1, and their sum
 // tells when they do.  Only when a row's sum passes kRaise is its maximum
 // found, m raised, O rescaled and the tile done again: fp32 and bf16 keep
@@ -323,6 +327,13 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
     const uint32_t ts = lanes + stream * 128, to = lanes + kTmemO + stream * D;
     const bool negative = a.scale_log2 < 0.0f;
     const float c = fabsf(a.scale_log2);
+    QuadRows rows;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        rows.token[u] = ((r & ~3) + u) / a.G;
+        rows.row[u] = rows.token[u] * a.Hq + ((r & ~3) + u) - rows.token[u] * a.G;
+    }
+    const int my_token = r / a.G;
     uint32_t phase = 0, done = 0;                    // of s_full and o_full
     for (uint32_t k = 0;; ++k) {
         const int slot = k % kItemSlots;
@@ -339,7 +350,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
         const int kt0 = sh.ring.item[slot].kt0, kt1 = sh.ring.item[slot].kt1;
         const int masked_from = (int)dense_masked_from(sh.ring.item[slot].first_pos);
         // tokens that the row sees from tile kt0 on
-        int64_t left = sh.ring.item[slot].first_pos + first + r / a.G + 1 - (int64_t)kt0 * kDenseTile;
+        int64_t left = sh.ring.item[slot].first_pos + first + my_token + 1 - (int64_t)kt0 * kDenseTile;
         float m = -INFINITY, l = 0.0f;               // m in units of S
         for (int kt = kt0; kt < kt1; ++kt, left -= kDenseTile) {
             if (!warp_wait(&sh.s_full[stream], phase & 1, a.ctrl, lane))
@@ -353,7 +364,8 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
 #pragma unroll 1
             for (int again = 0; again < 2; ++again) {
                 if (__any_sync(0xffffffffu, raise)) {
-                    const float top = tile_top(ts, negative, limit);
+                    // (to begin with, 32 scores that the row sees are enough)
+                    const float top = tile_top(ts, negative, limit, kt == kt0 && kt < masked_from && !again ? 1 : 4);
                     float f = 1.0f;
                     if (raise && top > m) {
                         f = ex2((m - top) * c);
@@ -376,7 +388,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
                 sum = kt >= masked_from ? tile_weights<true>(ts, m, c, negative, limit, p)
                                         : tile_weights<false>(ts, m, c, negative, limit, p);
                 raise = sum > kRaise;
-                if (kt == kt0 || !__any_sync(0xffffffffu, raise))
+                if (!__any_sync(0xffffffffu, raise))
                     break;
             }
             l += sum;
@@ -392,7 +404,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
             return;
         ++done;
         tmem_fence_after();
-        finish_row<D>(a, sh.ring.item[slot], sh.bad[slot] != 0, stream, r, lane, to, m * c, l);
+        finish_row<D>(a, sh.ring.item[slot], sh.bad[slot] != 0, stream, r, lane, rows, to, m * c, l);
         tmem_fence_before();
         __syncwarp();
         if (lane == 0)

@@ -66,6 +66,7 @@ int main()
         a.single = (int)pick(0, 1);
         a.TT = a.single ? 1 : 2 * (128 / a.G);
         a.split = pick(0, 3) != 0;
+        a.item_cost = (int)pick(64, 600);
         gridDim.x = (unsigned)(pick(0, 4) ? pick(1, 148) : 1);
         std::vector<int64_t> start(B + 1, 0);
         for (int b = 0; b < B; ++b) {
