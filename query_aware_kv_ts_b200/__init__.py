@@ -352,11 +352,14 @@ def ts_quest_select(kv: KVCache, scores, page_size: int, k: int, n_sink: int, n_
 # ---- new tokens of many requests: room, cache rows, attention ----
 
 # These calls bring few tokens at a time, so what the binding itself costs
-# counts: each check is one comparison where it holds, and says what is wrong
-# only where it does not.
+# counts: one expression says whether every argument is as it has to be, and
+# only where it is not are they looked at one by one, to say what is wrong.
 
-def _address(name, t, dtype, device: int, shape) -> int:
-    """The address of a contiguous tensor of this type and shape on the
+_I64, _BF16 = torch.int64, torch.bfloat16
+
+
+def _refuse(name, t, dtype, device: int, shape):
+    """Raises where t is not a contiguous tensor of this type and shape on the
     current CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
@@ -366,9 +369,8 @@ def _address(name, t, dtype, device: int, shape) -> int:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have the shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
-    return t.data_ptr()
 
 
 def _wrong_device(name, t, device: int):
@@ -384,20 +386,22 @@ def _token_rows(name, t, heads: int, d: int, device: int) -> int:
         raise TypeError("%s must be a torch tensor" % name)
     if t.get_device() != device:
         _wrong_device(name, t, device)
-    if t.dtype is not torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError("%s must be bf16" % name)
-    shape = t.shape
+    shape, st = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError("%s must be [tokens, %d, %d] (got %s)" % (name, heads, d, tuple(shape)))
-    st = t.stride()
     if shape[0] and (st[2] != 1 or (heads > 1 and st[1] != d)):
         raise ValueError("%s must have contiguous heads of contiguous channels" % name)
     return st[0] if shape[0] > 1 else heads * d
 
 
-def _cache_on(kv: KVCache, device: int):
-    if kv.k.get_device() != device:
-        _wrong_device("the cache", kv.k, device)
+def _device_of(kv: KVCache) -> int:
+    """The current device, which has to hold the cache."""
+    dev = kv.k.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _wrong_device("the cache", kv.k, -1 if dev < 0 else torch.cuda.current_device())
+    return dev
 
 
 def _raw_stream(stream, device: int) -> int:
@@ -419,32 +423,45 @@ def ts_extend_pages(cached, fresh, page_size: int, free_pages, pool_pages: int, 
     lengths: cached, fresh int64 [B]; free_pages int32; page_table int32
     [B, stride], its new entries written; seq_offsets, q_offsets int64 [B+1],
     slots int64 [at least the new tokens] and pages_used int64 [1] written."""
-    if not isinstance(cached, torch.Tensor) or not cached.is_cuda:
-        raise ValueError("libts computes on the GPU only; cached must be a CUDA tensor")
-    if cached.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != cached.shape[0]:
-        raise ValueError("cached must be [batch] and page_table [batch, stride]")
-    dev, B, i64 = torch.cuda.current_device(), cached.shape[0], torch.int64
-    n_free, n_slots, stride = free_pages.numel(), slots.numel(), page_table.shape[1]
+    if not cached.is_cuda:
+        _wrong_device("cached", cached, -1)
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    n_free, n_slots, table = free_pages.numel(), slots.numel(), page_table.shape
+    B, stride = cached.numel(), table[-1]
+    if not (cached.dtype is _I64 and fresh.dtype is _I64 and seq_offsets.dtype is _I64 and q_offsets.dtype is _I64 and
+            slots.dtype is _I64 and pages_used.dtype is _I64 and free_pages.dtype is i32 and page_table.dtype is i32 and
+            cached.get_device() == dev and fresh.get_device() == dev and seq_offsets.get_device() == dev and
+            q_offsets.get_device() == dev and slots.get_device() == dev and pages_used.get_device() == dev and
+            free_pages.get_device() == dev and page_table.get_device() == dev and
+            cached.is_contiguous() and fresh.is_contiguous() and seq_offsets.is_contiguous() and
+            q_offsets.is_contiguous() and slots.is_contiguous() and pages_used.is_contiguous() and
+            free_pages.is_contiguous() and page_table.is_contiguous() and
+            fresh.numel() == B and seq_offsets.numel() == B + 1 and q_offsets.numel() == B + 1 and
+            pages_used.numel() == 1 and len(table) == 2 and table[0] == B):
+        for name, t, dtype, shape in (
+                ("cached", cached, _I64, (B,)), ("fresh", fresh, _I64, (B,)), ("seq_offsets", seq_offsets, _I64, (B + 1,)),
+                ("q_offsets", q_offsets, _I64, (B + 1,)), ("slots", slots, _I64, (n_slots,)),
+                ("pages_used", pages_used, _I64, (1,)), ("free_pages", free_pages, i32, (n_free,)),
+                ("page_table", page_table, i32, (B, stride))):
+            _refuse(name, t, dtype, dev, shape)
     _check(_lib.ts_extend_pages(
-        B, _address("cached", cached, i64, dev, (B,)), _address("fresh", fresh, i64, dev, (B,)), page_size,
-        _address("free_pages", free_pages, torch.int32, dev, (n_free,)), n_free, pool_pages,
-        _address("page_table", page_table, torch.int32, dev, (B, stride)), stride,
-        _address("seq_offsets", seq_offsets, i64, dev, (B + 1,)), _address("q_offsets", q_offsets, i64, dev, (B + 1,)),
-        _address("slots", slots, i64, dev, (n_slots,)), n_slots, _address("pages_used", pages_used, i64, dev, (1,)),
-        _raw_stream(stream, dev)))
+        B, cached.data_ptr(), fresh.data_ptr(), page_size, free_pages.data_ptr(), n_free, pool_pages,
+        page_table.data_ptr(), stride, seq_offsets.data_ptr(), q_offsets.data_ptr(), slots.data_ptr(), n_slots,
+        pages_used.data_ptr(), _raw_stream(stream, dev)))
 
 
 def ts_write_kv(kv: KVCache, k_new, v_new, slots, stream=None):
     """K and V rows of new tokens ([n, h_kv, d] bf16; views of a projection's
     output, of equal token stride) to the token rows slots (int64 [n]) of the
     cache; rows with a slot outside the cache go nowhere."""
-    dev = torch.cuda.current_device()
-    _cache_on(kv, dev)
+    dev = _device_of(kv)
     n, st = k_new.shape[0], _token_rows("k_new", k_new, kv.h_kv, kv.head_dim, dev)
     if _token_rows("v_new", v_new, kv.h_kv, kv.head_dim, dev) != st or v_new.shape[0] != n:
         raise ValueError("k_new and v_new must have the same shape and token stride")
+    if not (slots.dtype is _I64 and slots.get_device() == dev and slots.is_contiguous() and slots.numel() == n):
+        _refuse("slots", slots, _I64, dev, (n,))
     _check(_lib.ts_write_kv(kv.ref(), kv.struct.k, kv.struct.v, k_new.data_ptr(), v_new.data_ptr(), st,
-                            _address("slots", slots, torch.int64, dev, (n,)), n, _raw_stream(stream, dev)))
+                            slots.data_ptr(), n, _raw_stream(stream, dev)))
 
 
 def ts_dense_attn_workspace_bytes(kv: KVCache, q_offsets_host) -> int:
@@ -459,24 +476,27 @@ def ts_dense_attn(kv: KVCache, q, q_offsets_dev, q_offsets_host, out, lse, ws, s
     """Causal attention of each sequence's newest tokens (q [n, h_q, d] bf16,
     rows q_offsets[b] .. q_offsets[b+1] of sequence b) over all of its cached
     tokens; out bf16 [n, h_q, d], lse float32 [n, h_q] or None."""
-    dev = torch.cuda.current_device()
-    _cache_on(kv, dev)
+    dev = _device_of(kv)
     off = _host_offsets(q_offsets_host, kv.batch)
-    rows, h_q, d = int(off[-1]), kv.h_q, kv.head_dim
+    rows, h_q, d, B = int(off[-1]), kv.h_q, kv.head_dim, kv.batch
     st = _token_rows("q", q, h_q, d, dev)
     n_out = out.shape[0]
-    if q.shape[0] < rows or n_out < rows:
-        raise ValueError("q and out must hold the %d query rows" % rows)
-    if lse is not None:
-        if lse.shape[0] < rows:
-            raise ValueError("lse must hold the %d query rows" % rows)
-        lse = _address("lse", lse, torch.float32, dev, (lse.shape[0], h_q))
-    if ws.get_device() != dev:
+    if q.shape[0] < rows or n_out < rows or (lse is not None and lse.shape[0] < rows):
+        raise ValueError("q, out and lse must hold the %d query rows" % rows)
+    if not (q_offsets_dev.dtype is _I64 and out.dtype is _BF16 and q_offsets_dev.get_device() == dev and
+            out.get_device() == dev and ws.get_device() == dev and q_offsets_dev.is_contiguous() and
+            out.is_contiguous() and q_offsets_dev.numel() == B + 1 and out.shape == (n_out, h_q, d)):
+        _refuse("q_offsets_dev", q_offsets_dev, _I64, dev, (B + 1,))
+        _refuse("out", out, _BF16, dev, (n_out, h_q, d))
         _wrong_device("ws", ws, dev)
-    _check(_lib.ts_dense_attn(
-        kv.ref(), q.data_ptr(), st, _address("q_offsets_dev", q_offsets_dev, torch.int64, dev, (kv.batch + 1,)),
-        off.__array_interface__["data"][0], _address("out", out, torch.bfloat16, dev, (n_out, h_q, d)), lse,
-        ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, dev)))
+    if lse is not None:
+        if not (lse.dtype is torch.float32 and lse.get_device() == dev and lse.is_contiguous() and
+                lse.shape == (lse.shape[0], h_q)):
+            _refuse("lse", lse, torch.float32, dev, (lse.shape[0], h_q))
+        lse = lse.data_ptr()
+    _check(_lib.ts_dense_attn(kv.ref(), q.data_ptr(), st, q_offsets_dev.data_ptr(), off.__array_interface__["data"][0],
+                              out.data_ptr(), lse, ws.data_ptr(), ws.numel() * ws.element_size(),
+                              _raw_stream(stream, dev)))
 
 
 def ts_status_string(status: int) -> str:

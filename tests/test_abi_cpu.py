@@ -290,11 +290,11 @@ def test_binding_refuses_host_tensors_and_wrong_types_of_new_tokens():
     with pytest.raises(TypeError, match="torch tensor"):
         ts._token_rows("q", [1.0], 2, 64, 0)
     with pytest.raises(ValueError, match="GPU only"):
-        ts._address("slots", i64, torch.int64, 0, (1,))
+        ts._refuse("slots", i64, torch.int64, 0, (1,))
     # (a host tensor's device is -1: the checks behind the device's)
     for t, dtype, shape in ((i64, torch.int32, (1,)), (rows[:, 0], torch.bfloat16, (4, 64)), (i64, torch.int64, (2,))):
         with pytest.raises((TypeError, ValueError), match="must"):
-            ts._address("t", t, dtype, -1, shape)
+            ts._refuse("t", t, dtype, -1, shape)
     for t in (rows.float(), rows[0], rows[:, :1], rows.transpose(0, 1), rows[:, :, ::2]):
         with pytest.raises((TypeError, ValueError), match="must"):
             ts._token_rows("t", t, 2, 64, -1)

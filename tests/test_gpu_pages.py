@@ -201,3 +201,40 @@ def test_rows_past_two_to_the_31_elements():
     torch.cuda.synchronize()
     assert (k[-1] == 1).all() and (v[-1] == 2).all() and (k[-2] == 0).all()
     assert float(k.sum(dtype=torch.float64)) == h_kv * d
+
+
+def test_the_binding_refuses_what_the_kernels_could_not_read():
+    """Wrong types, sizes, strides and devices, told by name, before any launch."""
+    m = H.ts()
+    c = case(3, 16, 100, 50, 1)
+    _, good = extend(*c)
+    t = torch.zeros
+    for at, bad in ((0, good[0].int()), (1, good[1][:2]), (3, good[3].long()), (5, good[5].t()), (5, good[5][:2]), (6, good[6][:3]),
+                    (7, good[7].cpu()), (8, t(40, dtype=torch.int64, device="cuda")[::2]), (8, good[8].float()),
+                    (9, t(2, dtype=torch.int64, device="cuda")), (9, [0])):
+        args = list(good)
+        args[at] = bad
+        with pytest.raises((TypeError, ValueError, AttributeError)):
+            m.ts_extend_pages(*args)
+    k = t((32, 2, 64), dtype=torch.bfloat16, device="cuda")
+    kv, new = m.KVCache(k, k.clone(), [0, 32], 2), t((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    slots = t(4, dtype=torch.int64, device="cuda")
+    for args in ((new, new, slots.int()), (new, new, slots[:3]), (new, new[:3], slots), (new.float(), new, slots),
+                 (new, new.cpu(), slots), (new[:, :1], new[:, :1], slots), (new, torch.cat([new, new], 1)[:, :2], slots),
+                 (new.transpose(1, 2), new, slots), (new, new, slots.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            m.ts_write_kv(kv, *args)
+    buf = m.DenseBuffers(kv, [0, 4])
+    ok = (kv, new, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
+    for at, bad in ((1, new[:3]), (1, new.float()), (2, buf.q_offsets_dev.int()), (2, buf.q_offsets_dev[:1]), (3, [0, 1, 2]),
+                    (4, buf.out.float()), (4, buf.out[:3]), (4, torch.cat([buf.out, buf.out], 1)[:, :2]), (5, buf.lse[:3]),
+                    (5, buf.lse.double()), (6, buf.ws.cpu())):
+        args = list(ok)
+        args[at] = bad
+        with pytest.raises((TypeError, ValueError)):
+            m.ts_dense_attn(*args)
+    with pytest.raises(m.TsError) as e:
+        m.ts_dense_attn(*ok[:6], buf.ws[:16])
+    assert e.value.status == m.TS_ERR_WORKSPACE
+    with pytest.raises(m.TsError, match="non-decreasing"):
+        m.ts_dense_attn(*ok[:3], [0, -1], *ok[4:])
