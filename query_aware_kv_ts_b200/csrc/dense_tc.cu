@@ -351,6 +351,8 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
         const int masked_from = (int)dense_masked_from(sh.ring.item[slot].first_pos);
         // tokens that the row sees from tile kt0 on
         int64_t left = sh.ring.item[slot].first_pos + first + my_token + 1 - (int64_t)kt0 * kDenseTile;
+        // (rows without a token hold anything: they never have the tile done again)
+        const bool live = my_token < min(kStreamRows / a.G, sh.ring.item[slot].tokens - first);
         float m = -INFINITY, l = 0.0f;               // m in units of S
         for (int kt = kt0; kt < kt1; ++kt, left -= kDenseTile) {
             if (!warp_wait(&sh.s_full[stream], phase & 1, a.ctrl, lane))
@@ -358,7 +360,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
             ++phase;
             tmem_fence_after();
             const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
-            bool raise = kt == kt0 || m == -INFINITY;   // no reference yet
+            bool raise = live && m == -INFINITY;     // no reference yet
             uint32_t p[kDenseTile / 2];
             float sum = 0.0f;
 #pragma unroll 1
@@ -387,7 +389,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
                 }
                 sum = kt >= masked_from ? tile_weights<true>(ts, m, c, negative, limit, p)
                                         : tile_weights<false>(ts, m, c, negative, limit, p);
-                raise = sum > kRaise;
+                raise = live && sum > kRaise;
                 if (!__any_sync(0xffffffffu, raise))
                     break;
             }
