@@ -277,7 +277,9 @@ __device__ __forceinline__ float tile_weights(uint32_t ts, float m, float c, boo
     for (int x = 0; x < kDenseTile / 32; ++x) {
         float s[32];
         load_scores(ts + x * 32, negative, s);
-        if (MASKED) {
+        // (the 32 rows of a warp have few tokens: most of a masked tile's
+        // scores are seen by all or none)
+        if (MASKED && !__all_sync(0xffffffffu, limit >= (x + 1) * 32)) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
                 s[e] = x * 32 + e < limit ? s[e] : -INFINITY;
@@ -367,7 +369,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
             for (int again = 0; again < 2; ++again) {
                 if (__any_sync(0xffffffffu, raise)) {
                     // (to begin with, 32 scores that the row sees are enough)
-                    const float top = tile_top(ts, negative, limit, kt == kt0 && kt < masked_from && !again ? 1 : 4);
+                    const float top = tile_top(ts, negative, limit, kt == kt0 && !again ? 1 : 4);
                     float f = 1.0f;
                     if (raise && top > m) {
                         f = ex2((m - top) * c);
