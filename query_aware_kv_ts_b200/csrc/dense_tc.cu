@@ -353,8 +353,6 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
         const int masked_from = (int)dense_masked_from(sh.ring.item[slot].first_pos);
         // tokens that the row sees from tile kt0 on
         int64_t left = sh.ring.item[slot].first_pos + first + my_token + 1 - (int64_t)kt0 * kDenseTile;
-        // (rows without a token hold anything: they never have the tile done again)
-        const bool live = my_token < min(kStreamRows / a.G, sh.ring.item[slot].tokens - first);
         float m = -INFINITY, l = 0.0f;               // m in units of S
         for (int kt = kt0; kt < kt1; ++kt, left -= kDenseTile) {
             if (!warp_wait(&sh.s_full[stream], phase & 1, a.ctrl, lane))
@@ -362,7 +360,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
             ++phase;
             tmem_fence_after();
             const int limit = left < 0 ? 0 : (left < kDenseTile ? (int)left : kDenseTile);
-            bool raise = live && m == -INFINITY;     // no reference yet
+            bool raise = m == -INFINITY;             // no reference yet
             uint32_t p[kDenseTile / 2];
             float sum = 0.0f;
 #pragma unroll 1
@@ -391,7 +389,7 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
                 }
                 sum = kt >= masked_from ? tile_weights<true>(ts, m, c, negative, limit, p)
                                         : tile_weights<false>(ts, m, c, negative, limit, p);
-                raise = live && sum > kRaise;
+                raise = sum > kRaise;
                 if (!__any_sync(0xffffffffu, raise))
                     break;
             }
@@ -640,6 +638,18 @@ dense_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
     }
     if (warp == kMmaWarp)
         tmem_alloc(&sh.tmem, kTmemCols);
+    // the query rows that no load fills (126 of 128 have a token with 7 heads a
+    // group): what lay there would make scores of any size, and a reference
+    // raised at every tile
+    if (warp < 4) {
+        const int pad = kStreamRows / a.G * a.G;
+        for (int i = tid; i < 2 * (D / 64) * (kStreamRows - pad) * 8; i += 128) {
+            const int row = i >> 3, block = row / (kStreamRows - pad);
+            *reinterpret_cast<uint4 *>(sq + block * (kStreamRows * 128) + (pad + row % (kStreamRows - pad)) * 128 +
+                                       (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+    }
     if (warp == kLoadWarp && lane < 3)
         tma_prefetch_desc(lane == 0 ? &qmap : (lane == 1 ? &kmap : &vmap));
     pdl_wait();
