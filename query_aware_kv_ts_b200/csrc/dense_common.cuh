@@ -588,15 +588,23 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
                     }
                     __syncwarp();
                 } else {
-#pragma unroll 4
-                    for (int p = 0; p < 1 << log_pages; ++p) {
-                        const int32_t y = __shfl_sync(0xffffffffu, row, (done << log_pages) + p);
+#pragma unroll 1
+                    for (int p0 = 0; p0 < 1 << log_pages; p0 += 4) {
+                        int32_t y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = __shfl_sync(0xffffffffu, row, (done << log_pages) + p0 + i);
                         if (elect_one()) {
-                            const uint32_t to = dst + ((p * D * 2) << a.box_shift);
-                            if (D == 128)
-                                tma_load_page(to, map, bar, y >> 3, g);
-                            else
-                                tma_load_tile(to, map, bar, 0, y, g);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i > 0 && p0 + i >= 1 << log_pages)
+                                    break;
+                                const uint32_t to = dst + (((p0 + i) * D * 2) << a.box_shift);
+                                if (D == 128)
+                                    tma_load_page(to, map, bar, y[i] >> 3, g);
+                                else
+                                    tma_load_tile(to, map, bar, 0, y[i], g);
+                            }
                         }
                         __syncwarp();
                     }
