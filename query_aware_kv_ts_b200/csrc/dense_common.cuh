@@ -589,14 +589,14 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
                     __syncwarp();
                 } else {
 #pragma unroll 1
-                    for (int p0 = 0; p0 < 1 << log_pages; p0 += 4) {
-                        int32_t y[4];
+                    for (int p0 = 0; p0 < 1 << log_pages; p0 += 8) {
+                        int32_t y[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 8; ++i)
                             y[i] = __shfl_sync(0xffffffffu, row, (done << log_pages) + p0 + i);
                         if (elect_one()) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 8; ++i) {
                                 if (i > 0 && p0 + i >= 1 << log_pages)
                                     break;
                                 const uint32_t to = dst + (((p0 + i) * D * 2) << a.box_shift);
