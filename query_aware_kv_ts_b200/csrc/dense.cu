@@ -31,12 +31,21 @@ dense_merge(const DenseArgs a, int blocks)
     const DensePiece p = a.pieces[c];
     if (!(p.flags & kPieceHead))
         return;
+    int last = c + 1;                                // the first block behind c that is not wholly inside the item
+    for (;; last += 32) {
+        const uint32_t vote = __ballot_sync(
+            0xffffffffu, last + lane >= blocks - 1 || !(a.pieces[last + lane].flags & kPieceThrough));
+        if (vote) {
+            last += __ffs(vote) - 1;
+            break;
+        }
+    }
     const int T = kStreamRows / a.G;
     const int64_t f = a.q_off[p.b + 1] - a.q_off[p.b], q_row = a.q_off[p.b] + (int64_t)p.t * a.TT;
     const int tokens = (int)min((int64_t)a.TT, f - (int64_t)p.t * a.TT);
     for (int i = blockIdx.y * kMergeWarps + warp; i < tokens * a.G; i += gridDim.y * kMergeWarps) {
         const int token = i / a.G, head = i - token * a.G;
-        dense_join_row<D>(a, p.b, p.g, p.t, c, blocks, token / T * kStreamRows + (token % T) * a.G + head,
+        dense_join_row<D>(a, c, last, token / T * kStreamRows + (token % T) * a.G + head,
                           (q_row + token) * a.Hq + p.g * a.G + head, lane);
     }
 }
@@ -110,7 +119,6 @@ ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, 
     a.Hq = p.Hq;
     a.Hkv = p.Hkv;
     a.G = p.G;
-    a.scale = p.scale;
     a.scale_log2 = p.scale * kLog2e;
     a.page_table = p.paged ? kv->page_table_dev : nullptr;
     a.pt_stride = kv->page_table_stride;

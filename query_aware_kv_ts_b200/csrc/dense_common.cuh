@@ -5,12 +5,13 @@
 // query heads of one kv head, against the tokens that the last of them sees.
 // The items of the whole call stand in one line, sequence by sequence, kv
 // head by kv head, each as long as its tokens plus a constant, and block c
-// takes the c-th of gridDim.x equal parts of that line.  Parts end inside
-// items, at a multiple of kDenseTile tokens; the pieces of such an item are
-// joined by dense_merge.  So blocks are equally loaded at any mixture of
-// lengths, and one long sequence spreads over the whole GPU.  Everything
-// follows from the device's offsets in closed form: no atomics, no order
-// that changes from run to run.
+// takes the c-th of as many equal parts of that line as there are blocks (of
+// fewer, where parts would be shorter than a tile).  Parts end inside items,
+// at a multiple of kDenseTile tokens; the pieces of such an item are joined in
+// their order.  So blocks are equally loaded at any mixture of lengths, and
+// one long sequence spreads over the whole GPU.  Everything follows from the
+// device's offsets in closed form, and no result depends on which block comes
+// first.
 #pragma once
 
 #include "ts_device.cuh"
@@ -30,7 +31,6 @@ struct __align__(16) DensePiece {
 enum : int32_t {
     kPieceHead = 1,      // the block begins an item that it does not end
     kPieceThrough = 2,   // the block lies wholly inside an item: neither begins nor ends it
-    kPieceEmpty = 4,     // and holds no tile of it
 };
 
 struct DenseArgs {
@@ -49,8 +49,8 @@ struct DenseArgs {
     int item_cost;        // what an item's beginning and end take, in tokens of its tiles
     double inv_grid;      // 1 / blocks
     int slot_rows;        // rows of one partial result
-    uint32_t *counts;     // [grid][8], zero between calls: tiles done of the items that blocks share
-    float scale, scale_log2;
+    uint32_t *counts;     // [grid][8], zero between calls: of the item that a block begins and does not end
+    float scale_log2;
     // paged cache (page_table != null): token i of sequence b is pool row
     // page_table[b * pt_stride + (i >> page_shift)] << page_shift | (i & (page - 1))
     const int32_t *page_table;
@@ -74,7 +74,7 @@ struct DenseItem {
     int64_t off, n, first_pos; // the sequence's first row and length; position of its first query token
     int64_t line;              // the sequence's beginning on the line, and its query tokens
     int32_t f;
-    int32_t counter;           // dense_counter, of a shared item
+    int32_t head;              // of a shared item, the block that begins it
 };
 
 __device__ __forceinline__ int64_t seq_items(const DenseArgs &a, int64_t f)
@@ -153,10 +153,37 @@ struct DenseTables {
     int64_t *start, *seq_off, *q_off;
 };
 
-// Where part c begins on the line (part gridDim.x: its end).
-__device__ __forceinline__ int64_t dense_part(const DenseArgs &a, int64_t total, int c)
+// The line cut into parts, none shorter than a tile: so a part inside an item
+// holds a tile of it.
+struct DenseParts {
+    int64_t total;
+    int32_t count;
+    double inverse;
+
+    __device__ __forceinline__ void cut(const DenseArgs &a, int64_t length)
+    {
+        total = length;
+        const int64_t most = length / (kDenseTile + 1);   // (1 for at()'s rounding)
+        count = most < (int64_t)gridDim.x ? (most > 1 ? (int32_t)most : 1) : (int32_t)gridDim.x;
+        inverse = count == (int32_t)gridDim.x ? a.inv_grid : 1.0 / count;
+    }
+    // Where part c begins.
+    __device__ __forceinline__ int64_t at(int c) const
+    {
+        return c >= count ? total : (int64_t)((double)total * c * inverse);
+    }
+};
+
+// The tile of an item of `cost` at which a part that ends rem after the item's
+// beginning is cut (its number of tiles: behind it).
+__device__ __forceinline__ int32_t dense_cut(const DenseArgs &a, int64_t rem, int64_t cost, int32_t tiles)
 {
-    return c >= (int)gridDim.x ? total : (int64_t)((double)total * c * a.inv_grid);
+    if (!a.split)
+        return 2 * rem < cost ? 0 : tiles;
+    const int64_t c = rem < a.item_cost - kDenseTile / 2 ? 0 : (rem - a.item_cost + kDenseTile / 2) / kDenseTile;
+    if (c >= tiles || (tiles >= 8 && c > tiles - 2))
+        return tiles;
+    return tiles >= 8 && c < 2 ? 0 : (int32_t)c;     // no piece of a single tile
 }
 
 __device__ __forceinline__ void dense_table_seq(const DenseTables &tab, DensePlace &p)
@@ -205,19 +232,7 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const Den
     p.t = (int32_t)t0;
     rem -= items_cost(a, base, t0);
     dense_item_at(a, p);
-    if (a.split) {
-        const int32_t c = rem < a.item_cost - kDenseTile / 2 ? 0
-                              : (int32_t)((rem - a.item_cost + kDenseTile / 2) / kDenseTile);
-        p.cut = c < p.tiles ? c : p.tiles;
-        if (p.tiles >= 8) {                    // no piece of a single tile
-            if (p.cut < 2)
-                p.cut = 0;
-            else if (p.cut > p.tiles - 2)
-                p.cut = p.tiles;
-        }
-    } else {
-        p.cut = 2 * rem < base + (t0 + 1) * a.TT + a.item_cost ? 0 : p.tiles;
-    }
+    p.cut = dense_cut(a, rem, base + (t0 + 1) * a.TT + a.item_cost, p.tiles);
     if (p.cut == p.tiles) {                    // the next item's beginning
         p.cut = 0;
         if (++p.t == items) {
@@ -241,7 +256,7 @@ __device__ __forceinline__ DensePlace dense_locate(const DenseArgs &a, const Den
 // false at the end.  All lanes of a warp walk alike.
 struct DenseWalk {
     DensePlace at, end;
-    int64_t total;                                          // the line's length
+    DenseParts parts;
 
     __device__ __forceinline__ bool same_item() const { return at.b == end.b && at.g == end.g && at.t == end.t; }
     // For dense_merge; call it before next().
@@ -253,8 +268,6 @@ struct DenseWalk {
         p.t = end.t;
         const bool inside = end.b < a.B && end.cut > 0;     // the part ends inside an item
         p.flags = inside ? (same_item() && at.cut > 0 ? kPieceThrough : kPieceHead) : 0;
-        if (inside && same_item() && at.cut == end.cut)
-            p.flags = kPieceThrough | kPieceEmpty;
         return p;
     }
     __device__ __forceinline__ bool next(const DenseArgs &a, DenseItem &it)
@@ -286,17 +299,20 @@ struct DenseWalk {
     }
 };
 
-// A number below gridDim.x of each shared item's own, the same for all its
-// pieces: the part in which it begins (an item that a part's end cuts is the
-// last to begin in its part).
-__device__ __forceinline__ int32_t dense_counter(const DenseArgs &a, const DenseItem &it, int64_t total)
+// The block that begins a shared item.
+__device__ __forceinline__ int32_t dense_head(const DenseArgs &a, const DenseItem &it, const DenseParts &parts)
 {
+    if (it.kt0 == 0)
+        return (int32_t)blockIdx.x;
     const int64_t base = it.n > it.f ? it.n - it.f : 0;
     const int64_t x = it.line + it.g * items_cost(a, base, seq_items(a, it.f)) + items_cost(a, base, it.t);
-    int c = min((int)((float)x * (float)gridDim.x / (float)total), (int)gridDim.x - 1);
-    while (dense_part(a, total, c) > x)
+    int c = min((int)((float)x * (float)parts.count / (float)parts.total), parts.count - 1);
+    while (parts.at(c) > x)
         --c;
-    while (dense_part(a, total, c + 1) <= x)
+    while (parts.at(c + 1) <= x)
+        ++c;
+    // a part that ends too near the item's beginning ends there
+    while (dense_cut(a, parts.at(c + 1) - x, base + (it.t + 1) * (int64_t)a.TT + a.item_cost, it.tiles) == 0)
         ++c;
     return c;
 }
@@ -343,9 +359,9 @@ __device__ __forceinline__ void dense_begin(const DenseArgs &a, void *smem, int 
     if (lane == 0)
         tab.start[0] = 0;
     __syncwarp();
-    w.total = tab.start[a.B];
+    w.parts.cut(a, tab.start[a.B]);
     if (lane < 2)
-        place[lane] = dense_locate(a, tab, dense_part(a, w.total, (int)blockIdx.x + lane));
+        place[lane] = dense_locate(a, tab, w.parts.at((int)blockIdx.x + lane));
     __syncwarp();
     w.at = place[0];
     w.end = place[1];
@@ -565,9 +581,9 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
                 // (wanted at the item's end only; written before the arrival
                 // for its first V tile, it is there by then)
                 if (kv == 1 && kt == kt0 && it.slot >= 0 && !QL) {
-                    const int32_t c = dense_counter(a, it, w.total);
+                    const int32_t c = dense_head(a, it, w.parts);
                     if (elect_one())
-                        r.item[slot].counter = c;
+                        r.item[slot].head = c;
                     __syncwarp();
                 }
                 const int st = n % NS;
@@ -625,46 +641,29 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     }
 }
 
-// Whole warp: one row of an item that several blocks share.  The block that
-// begins it (the first from `from` on that says so) has its first piece (slot
-// 2 c + 1), each further block the rest of its part (slot 2 q; some hold
-// none), up to the first that is not wholly inside the item.  With (m_p, l_p,
-// O_p) a piece's maximum in base 2, sum and weighted sum, and M = max m_p:
+// Whole warp: one row of an item that the blocks head to last share: head has
+// its first piece (slot 2 c + 1), each further block the next (slot 2 q).
+// With (m_p, l_p, O_p) a piece's maximum in base 2, sum and weighted sum, and
+// M = max m_p:
 //   O = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
-// in piece order, to row `at` (query row x head) of the output.  32 blocks'
-// pieces a round trip.
+// in piece order, to row `at` (query row x head) of the output.  32 pieces a
+// round trip.
 template <int D>
-__device__ __forceinline__ void dense_join_row(const DenseArgs &a, int b, int g, int t, int from, int blocks, int row,
-                                               int64_t at, int lane)
+__device__ __forceinline__ void dense_join_row(const DenseArgs &a, int head, int last, int row, int64_t at, int lane)
 {
     constexpr int PS = D + 4, C = D / 32;
-    int4 p;
-    uint32_t vote;
-    for (;; from += 32) {                            // (at the first place, but where parts hold less than a tile)
-        p = make_int4(-1, 0, 0, 0);
-        if (from + lane < blocks)
-            p = __ldcg(reinterpret_cast<const int4 *>(a.pieces + from + lane));
-        vote = __ballot_sync(0xffffffffu, (p.x == b && p.y == g && p.z == t && (p.w & kPieceHead)) ||
-                                              from + lane >= blocks);
-        if (vote)
-            break;
-    }
-    const int head = from + __ffs(vote) - 1;
+    auto piece = [&](int q) {
+        return a.part + ((int64_t)(q == head ? 2 * q + 1 : 2 * q) * a.slot_rows + row) * PS;
+    };
     float M = -INFINITY, L = 0.0f, acc[C];
 #pragma unroll
     for (int e = 0; e < C; ++e)
         acc[e] = 0.0f;
-    for (int q0 = head; q0 < blocks;) {
-        // this round's pieces: the blocks q0 + lane of the item that hold some
-        const int q = q0 + lane;
-        const int flags = q < blocks ? __ldcg(&a.pieces[q].flags) : 0;
-        const uint32_t ends = __ballot_sync(0xffffffffu, q != head && !(flags & kPieceThrough));
-        const int count = ends ? __ffs(ends) : 32;   // the block that ends the item has the last
-        const bool holds = lane < count && q < blocks && (q == head || !(flags & kPieceEmpty));
-        const float *mine = a.part + ((int64_t)(q == head ? 2 * q + 1 : 2 * q) * a.slot_rows + row) * PS;
+    for (int q0 = head; q0 <= last; q0 += 32) {
+        const int count = min(32, last - q0 + 1);
         float2 ml = make_float2(-INFINITY, 0.0f);
-        if (holds)
-            ml = __ldcg(reinterpret_cast<const float2 *>(mine + D));
+        if (lane < count)
+            ml = __ldcg(reinterpret_cast<const float2 *>(piece(q0 + lane) + D));
         float top = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -687,12 +686,11 @@ __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int b, int g,
             for (int j = 0; j < 8; ++j) {            // eight pieces' rows in flight
                 wj[j] = __shfl_sync(0xffffffffu, w, j0 + j);
                 L += __shfl_sync(0xffffffffu, l, j0 + j);
-                const int qj = q0 + j0 + j;
-                const float *src = a.part + ((int64_t)(qj == head ? 2 * qj + 1 : 2 * qj) * a.slot_rows + row) * PS;
 #pragma unroll
                 for (int e = 0; e < C / 2; ++e)
-                    x[j][e] = wj[j] != 0.0f ? __ldcg(reinterpret_cast<const float2 *>(src + lane * C) + e)
-                                            : make_float2(0.0f, 0.0f);
+                    x[j][e] = wj[j] != 0.0f
+                                  ? __ldcg(reinterpret_cast<const float2 *>(piece(q0 + j0 + j) + lane * C) + e)
+                                  : make_float2(0.0f, 0.0f);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -702,9 +700,6 @@ __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int b, int g,
                     acc[2 * e + 1] += wj[j] * x[j][e].y;
                 }
         }
-        if (ends)
-            break;
-        q0 += 32;
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll

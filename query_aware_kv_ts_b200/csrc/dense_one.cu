@@ -21,6 +21,7 @@ constexpr int kOneWarps = 8;
 constexpr int kOneThreads = (kOneWarps + 1) * 32;
 constexpr float kRaise = 8.0f;           // log2 of how far weights may grow before the sums are rescaled
 constexpr int kOneMaxStages = 10;
+constexpr int kCountTiles = 20;          // bits of the joins' counters that count tiles (4M tokens: 32768)
 
 template <int D, bool WIDE>
 constexpr int kJoinBytes = kOneWarps * (WIDE ? 16 : 8) * (D + 4) * 4;
@@ -192,7 +193,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
             if (lane == 0)
                 mbar_arrive(&sh.ring.empty[sv]);
         }
-        const int counter = sh.ring.item[slot].counter;
+        const int head = sh.ring.item[slot].head;
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.ring.item_empty[slot]);
@@ -270,20 +271,22 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
         }
         // A shared item's rows are joined by whichever block's warp comes last
         // (the sum is taken in piece order, whoever that is): each adds its
-        // tiles to the rows' counter and goes on.
+        // tiles to the rows' counter and goes on, the block that ends the item
+        // also its own number, so that the last one knows the blocks between.
         if (part_slot >= 0 && warp < a.G) {
-            uint32_t *count = a.counts + counter * 8 + warp;
+            uint32_t *count = a.counts + head * 8 + warp;
+            const uint32_t mine = (uint32_t)(kt1 - kt0) + (kt1 == tiles ? (blockIdx.x + 1u) << kCountTiles : 0u);
             __threadfence();
             __syncwarp();
-            uint32_t before = 0;
+            uint32_t sum = 0;
             if (lane == 0)
-                before = atomicAdd(count, (uint32_t)(kt1 - kt0));
-            before = __shfl_sync(0xffffffffu, before, 0);
-            if (before + (uint32_t)(kt1 - kt0) == (uint32_t)tiles) {
+                sum = atomicAdd(count, mine) + mine;
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            if ((sum & ((1u << kCountTiles) - 1u)) == (uint32_t)tiles) {
                 __threadfence();
 #pragma unroll 1
                 for (int row = warp; row < a.G; row += kOneWarps)
-                    dense_join_row<D>(a, b, g, 0, counter, (int)gridDim.x, row, q_row * a.Hq + g * a.G + row, lane);
+                    dense_join_row<D>(a, head, (int)(sum >> kCountTiles) - 1, row, q_row * a.Hq + g * a.G + row, lane);
                 if (lane == 0)
                     *count = 0u;                     // as the next call finds it
             }

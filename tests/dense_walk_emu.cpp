@@ -47,7 +47,7 @@ int main()
     std::mt19937_64 rng(7);
     auto pick = [&](int64_t lo, int64_t hi) { return lo + (int64_t)(rng() % (uint64_t)(hi - lo + 1)); };
     int cases = 0, failures = 0;
-    for (int trial = 0; trial < 6000; ++trial) {
+    for (int trial = 0; trial < 12000; ++trial) {
         const int B = (int)pick(1, trial % 7 == 0 ? 40 : 6);
         std::vector<int64_t> so(B + 1, 0), qo(B + 1, 0);
         const int64_t n_hi = trial % 3 == 0 ? 200 : (trial % 3 == 1 ? 5000 : 200000);
@@ -67,7 +67,7 @@ int main()
         a.TT = a.single ? 1 : 2 * (128 / a.G);
         a.split = pick(0, 3) != 0;
         a.item_cost = (int)pick(64, 600);
-        gridDim.x = (unsigned)(pick(0, 4) ? pick(1, 148) : 1);
+        gridDim.x = (unsigned)(pick(0, 4) ? (pick(0, 3) ? pick(1, 148) : 148) : 1);
         std::vector<int64_t> start(B + 1, 0);
         for (int b = 0; b < B; ++b) {
             const int64_t n = so[b + 1] - so[b], f = qo[b + 1] - qo[b];
@@ -77,7 +77,7 @@ int main()
         const DenseTables tab = {start.data(), so.data(), qo.data()};
         using Key = std::tuple<int, int, int>;
         struct Part {
-            int kt0, kt1, slot, tiles, tokens, counter;
+            int kt0, kt1, slot, tiles, tokens, head;
         };
         std::map<Key, std::vector<Part>> got;
         std::vector<DensePiece> pieces(gridDim.x);
@@ -85,9 +85,9 @@ int main()
         for (unsigned c = 0; c < gridDim.x; ++c) {
             blockIdx.x = c;
             DenseWalk w;
-            w.total = start[B];
-            w.at = dense_locate(a, tab, dense_part(a, w.total, (int)c));
-            w.end = dense_locate(a, tab, dense_part(a, w.total, (int)c + 1));
+            w.parts.cut(a, start[B]);
+            w.at = dense_locate(a, tab, w.parts.at((int)c));
+            w.end = dense_locate(a, tab, w.parts.at((int)c + 1));
             pieces[c] = w.piece(a);
             DenseItem it;
             while (w.next(a, it)) {
@@ -95,7 +95,7 @@ int main()
                 ok &= it.n == so[it.b + 1] - so[it.b];
                 ok &= it.first_pos == it.n - (qo[it.b + 1] - qo[it.b]) + (int64_t)it.t * a.TT;
                 got[Key(it.b, it.g, it.t)].push_back({it.kt0, it.kt1, it.slot, it.tiles, it.tokens,
-                                                          it.slot >= 0 ? dense_counter(a, it, w.total) : 0});
+                                                          it.slot >= 0 ? dense_head(a, it, w.parts) : -1});
             }
         }
         size_t items = 0;
@@ -126,8 +126,7 @@ int main()
                 continue;
             std::vector<int> slots{2 * (int)c + 1};
             for (unsigned q = c + 1; q < gridDim.x; ++q) {
-                if (!(pieces[q].flags & kPieceEmpty))
-                    slots.push_back(2 * (int)q);
+                slots.push_back(2 * (int)q);
                 if (!(pieces[q].flags & kPieceThrough))
                     break;
             }
@@ -143,15 +142,12 @@ int main()
             joined.erase(e.first);
         }
         ok &= joined.empty();
-        // the shared items' counters: one for all pieces, of each item its own
-        std::map<int, Key> counters;
+        // every piece knows the block that begins its item, which begins no other shared one
+        std::map<int, Key> heads;
         for (auto &e : got)
             for (const Part &p : e.second)
                 if (p.slot >= 0)
-                    ok &= p.counter >= 0 && p.counter < (int)gridDim.x &&
-                          counters.emplace(p.counter, e.first).first->second == e.first &&
-                          p.counter == e.second[0].counter &&
-                          (p.slot % 2 == 0 || p.slot / 2 >= p.counter);   // the join looks from there on
+                    ok &= 2 * p.head + 1 == e.second[0].slot && heads.emplace(p.head, e.first).first->second == e.first;
         ++cases;
         if (!ok && failures++ < 5)
             std::printf("failed: trial %d B %d Hkv %d G %d single %d split %d grid %u\n", trial, B, a.Hkv, a.G, a.single,

@@ -32,4 +32,4 @@ def test_every_tile_once_and_every_join(tmp_path):
     subprocess.run(["g++", "-std=c++20", "-O2", "-I", str(tmp_path), HARNESS, "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout
-    assert r.stdout.strip().endswith("6000 cases, 0 failures")
+    assert r.stdout.strip().endswith("12000 cases, 0 failures")

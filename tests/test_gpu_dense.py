@@ -362,3 +362,110 @@ def test_prompt_in_chunks_then_a_decode_step():
     torch.cuda.synchronize()
     assert torch.equal(got.ids, want.ids) and torch.equal(got.count, want.count)
     assert (got.out - want.out).abs().max() <= H.OUT_ATOL
+
+
+@pytest.mark.parametrize("fresh", [1, 100])
+def test_a_short_sequence_in_a_cache_with_room_for_a_long_one(fresh):
+    """The launch is sized for the capacity, the work for the current length."""
+    m = H.ts()
+    cap, h_q, h_kv, d = 200000, 28, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(12)
+    k, v = (torch.randn((cap, h_kv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((fresh, h_q, d), device="cuda", generator=g).to(torch.bfloat16)
+    kv = m.KVCache(k, v, [0, 50000], h_q, capacity=cap)
+    buf = m.DenseBuffers(kv, [0, fresh])
+    for n in (fresh, 129, 1000, 1027, 5003, 20011, 130000):
+        kv.seq_offsets_dev[1] = n
+        buf.out.fill_(float("nan"))
+        m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
+        torch.cuda.synchronize()
+        check([(k[:n], v[:n])], [0, fresh], q, buf.out, buf.lse)
+    assert m.ts_get_device_status(buf.ws) == (m.TS_OK, 0)
+
+
+def test_many_sequences():
+    """1024 sequences, some empty, some without queries, some of one token."""
+    rng = np.random.default_rng(5)
+    n = rng.integers(0, 60, 1024)
+    f = np.minimum(rng.choice([0, 1, 1, 1, 2, 7, 40], 1024), n)
+    n[700], f[700] = 3000, 1
+    n[333], f[333] = 900, 500
+    off, q_off, q, k, v = inputs(n, f, 8, 2, 64, 3)
+    buf = attend(k, v, off, q, q_off, 8)
+    check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
+    kp, vp, table = paged(k, v, off, 8, 2)
+    again = attend(kp, vp, off, q, q_off, 8, table=table, page=8)
+    check(sequences(k, v, off), q_off, q, again.out, again.lse)
+
+
+def test_one_workspace_for_several_shapes_and_graphs():
+    """Calls of different shapes take turns on one workspace, captured ones too."""
+    m = H.ts()
+    cases = [inputs([9000, 40], [1, 1], 28, 4, 128, 1), inputs([700], [700], 32, 8, 128, 2), inputs([3000] * 3, [1, 70, 1], 8, 1, 64, 3),
+             inputs([20000], [1], 32, 2, 128, 4)]
+    kvs = [m.KVCache(k, v, off, q.shape[1]) for off, _, q, k, v in cases]
+    bufs = [m.DenseBuffers(kv, c[1]) for kv, c in zip(kvs, cases)]
+    ws = torch.empty(max(b.ws.numel() for b in bufs), dtype=torch.uint8, device="cuda")
+    m.ts_workspace_init(ws)
+
+    def call(i):
+        b = bufs[i]
+        m.ts_dense_attn(kvs[i], cases[i][2], b.q_offsets_dev, b.q_offsets_host, b.out, b.lse, ws)
+
+    def checked(i):
+        torch.cuda.synchronize()
+        off, q_off, q, k, v = cases[i]
+        check(sequences(k, v, off), q_off, q, bufs[i].out, bufs[i].lse)
+        bufs[i].out.zero_()
+
+    for i in (0, 1, 2, 3, 2, 0, 3, 1, 0):
+        call(i)
+        checked(i)
+    s, graphs = torch.cuda.Stream(), []
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for i in range(len(cases)):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=s):
+                call(i)
+        for i in (3, 0, 2, 1, 0, 3):
+            graphs[i].replay()
+            s.synchronize()
+            checked(i)
+    assert m.ts_get_device_status(ws) == (m.TS_OK, 0)
+
+
+@pytest.mark.parametrize("fresh", [1, 40])
+def test_pages_past_two_to_the_31_elements(fresh):
+    m = H.ts()
+    rows, h_q, h_kv, d, page, n = 2 ** 21 + 1024, 32, 8, 128, 16, 500
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.full((rows, h_kv, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    pages = torch.randperm(rows // page, generator=torch.Generator().manual_seed(1))[:32]
+    pages[:16] = rows // page - 1 - torch.arange(16)          # the last ones among them
+    table = pages.to(torch.int32).view(1, -1).contiguous().cuda()
+    i = torch.arange(n)
+    at = (pages[i // page] * page + i % page).cuda()
+    kk, vv = (torch.randn((n, h_kv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    k[at], v[at] = kk, vv
+    q = torch.randn((fresh, h_q, d), device="cuda", generator=g).to(torch.bfloat16)
+    buf = attend(k, v, [0, n], q, [0, fresh], h_q, table=table, page=page)
+    check([(kk, vv)], [0, fresh], q, buf.out, buf.lse)
+
+
+def test_ragged_batches_at_random():
+    rng = np.random.default_rng(99)
+    for trial in range(25):
+        h_q, h_kv, d = HEADS[trial % len(HEADS)]
+        B = int(rng.integers(1, 9))
+        n = rng.integers(0, int(rng.choice([50, 700, 6000])), B)
+        f = np.array([int(rng.choice([0, 1, min(2, x), rng.integers(0, x + 1), x])) if x else int(rng.integers(0, 3)) for x in n])
+        off, q_off, q, k, v = inputs(n, f, h_q, h_kv, d, trial, peaked=trial % 3 == 0)
+        page = int(rng.choice([0, 8, 16, 32, 256]))
+        if page:
+            kp, vp, table = paged(k, v, off, page, trial)
+            buf = attend(kp, vp, off, q, q_off, h_q, table=table, page=page)
+        else:
+            buf = attend(k, v, off, q, q_off, h_q)
+        check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
