@@ -45,7 +45,7 @@ dense_merge(const DenseArgs a, int blocks)
     const int tokens = (int)min((int64_t)a.TT, f - (int64_t)p.t * a.TT);
     for (int i = blockIdx.y * kMergeWarps + warp; i < tokens * a.G; i += gridDim.y * kMergeWarps) {
         const int token = i / a.G, head = i - token * a.G;
-        dense_join_row<D>(a, c, last, token / T * kStreamRows + (token % T) * a.G + head,
+        dense_join_row<D, 4>(a, c, last, token / T * kStreamRows + (token % T) * a.G + head,
                           (q_row + token) * a.Hq + p.g * a.G + head, lane);
     }
 }

@@ -647,8 +647,8 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
 // M = max m_p:
 //   O = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
 // in piece order, to row `at` (query row x head) of the output.  32 pieces a
-// round trip.
-template <int D>
+// round trip, F pieces' rows in flight.
+template <int D, int F>
 __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int head, int last, int row, int64_t at, int lane)
 {
     constexpr int PS = D + 4, C = D / 32;
@@ -679,11 +679,11 @@ __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int head, int
         // (a maximum of -inf with a sum: every score seen was NaN)
         const float w = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - M);
         const float l = ml.y * w;
-        for (int j0 = 0; j0 < count; j0 += 8) {
-            float2 x[8][C / 2];
-            float wj[8];
+        for (int j0 = 0; j0 < count; j0 += F) {
+            float2 x[F][C / 2];
+            float wj[F];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {            // eight pieces' rows in flight
+            for (int j = 0; j < F; ++j) {
                 wj[j] = __shfl_sync(0xffffffffu, w, j0 + j);
                 L += __shfl_sync(0xffffffffu, l, j0 + j);
 #pragma unroll
@@ -693,7 +693,7 @@ __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int head, int
                                   : make_float2(0.0f, 0.0f);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < F; ++j)
 #pragma unroll
                 for (int e = 0; e < C / 2; ++e) {
                     acc[2 * e] += wj[j] * x[j][e].x;

@@ -286,7 +286,7 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                 __threadfence();
 #pragma unroll 1
                 for (int row = warp; row < a.G; row += kOneWarps)
-                    dense_join_row<D>(a, head, (int)(sum >> kCountTiles) - 1, row, q_row * a.Hq + g * a.G + row, lane);
+                    dense_join_row<D, 8>(a, head, (int)(sum >> kCountTiles) - 1, row, q_row * a.Hq + g * a.G + row, lane);
                 if (lane == 0)
                     *count = 0u;                     // as the next call finds it
             }
