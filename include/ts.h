@@ -381,10 +381,12 @@ TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, 
  *   lse[r,h]   = log sum_{j <= p} exp(scale * q[r,h,:] . K[b,j,h/G,:])
  * with r = q_offsets[b] + i.  f_b = n_b is a whole prompt, f_b = 1 a decode
  * step, f_b = 0 a sequence without queries; they may stand side by side.  A
- * row that sees nothing (p < 0) gives zeros and -inf.  The scores, the
- * running maximum and sum and the weighted sums are fp32; the weights are
- * rounded to bf16 for the product with V, and out at the end.  Tokens that a
- * row does not see have no effect on it, whatever their K and V hold.
+ * row that sees nothing (p < 0) gives zeros and -inf.  The scores, their
+ * reference and sum and the weighted sums are fp32; the weights are rounded to
+ * bf16 for the product with V (with f_b = 1 as a bf16 and its bf16 remainder),
+ * and out at the end.  Tokens that a row does not see have no effect on it,
+ * whatever their K and V hold.  The result of a call depends on its arguments
+ * only, bit for bit.
  *   q              device bf16 [q_offsets[batch]][h_q][head_dim], 16-byte
  *                  aligned, q_stride_tok elements (a multiple of 8, at least
  *                  h_q * head_dim) from token to token
@@ -394,7 +396,9 @@ TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, 
  *                  16-byte aligned; rows behind the last are left as they were
  *   lse            device float32 [q_offsets[batch]][h_q] or NULL
  *   ws             workspace of ts_dense_attn_workspace_bytes, initialised
- *                  once (ts_workspace_init); ts_get_device_status reads it
+ *                  once (ts_workspace_init) and used by no other entry point
+ *                  but ts_get_device_status, which reads it; one of the
+ *                  largest size serves calls of several shapes in turn
  * The cache may be packed, growing (capacity; the length is read on the
  * device) or paged (a table entry outside the pool: no access outside the
  * pool, results not defined).  At most 2^24 query rows.

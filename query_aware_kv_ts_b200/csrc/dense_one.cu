@@ -3,7 +3,13 @@
 // Bound by reading K and V once, so what counts is bytes in flight: one
 // persistent block per SM, a loading warp that keeps a ring of 32 KB tiles
 // filled by TMA (K and V in turn), and eight warps that take 16 tokens of
-// every tile each.  A warp keeps its own running maximum, sum and weighted
+// every tile each.  Measured: one token over 1,048,576 of 4 x 128, 2.1 GB,
+// 324-335 us (98-101 % of the copy rate); 32 requests of 8192 to 65536 tokens
+// of 8 x 128 on 16-token pages, 3.0 GB, 488 us (92 %; 8-token pages, whose
+// boxes of 2 KB cost their issue, half as long again).  A block alone reads
+// about 27 bytes a clock, so a small batch goes to as many as it has tiles
+// (4 requests of about 1000 tokens: 12.6 us, 3 us of them the kernel's start
+// to its first load).  A warp keeps its own running maximum, sum and weighted
 // sums, and the eight are joined at the end of the item, so nothing in the
 // loop waits for another warp.
 //
