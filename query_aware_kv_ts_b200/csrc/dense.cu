@@ -28,20 +28,21 @@ dense_merge(const DenseArgs a, int blocks)
     pdl_wait();
     pdl_launch_dependents();
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const DensePiece p = a.pieces[c];
+    const int4 piece = __ldcg(reinterpret_cast<const int4 *>(a.pieces + c));
+    const DensePiece p = {piece.x, piece.y, piece.z, piece.w};
     if (!(p.flags & kPieceHead))
         return;
     int last = c + 1;                                // the first block behind c that is not wholly inside the item
     for (;; last += 32) {
         const uint32_t vote = __ballot_sync(
-            0xffffffffu, last + lane >= blocks - 1 || !(a.pieces[last + lane].flags & kPieceThrough));
+            0xffffffffu, last + lane >= blocks - 1 || !(__ldcg(&a.pieces[last + lane].flags) & kPieceThrough));
         if (vote) {
             last += __ffs(vote) - 1;
             break;
         }
     }
     const int T = kStreamRows / a.G;
-    const int64_t f = a.q_off[p.b + 1] - a.q_off[p.b], q_row = a.q_off[p.b] + (int64_t)p.t * a.TT;
+    const int64_t q0 = __ldcg(a.q_off + p.b), f = __ldcg(a.q_off + p.b + 1) - q0, q_row = q0 + (int64_t)p.t * a.TT;
     const int tokens = (int)min((int64_t)a.TT, f - (int64_t)p.t * a.TT);
     for (int i = blockIdx.y * kMergeWarps + warp; i < tokens * a.G; i += gridDim.y * kMergeWarps) {
         const int token = i / a.G, head = i - token * a.G;

@@ -522,6 +522,7 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
     DenseWalk w;
     dense_begin(a, ring, lane, w);
     fence_proxy_async_smem();                        // the tables are read: tiles may go over them
+    fence_proxy_async_global();                      // and what the kernel before wrote is loaded
     if (lane == 0)
         a.pieces[blockIdx.x] = w.piece(a);
     uint32_t n = 0;                                  // tiles loaded (K and V count one each)

@@ -210,11 +210,12 @@ __device__ __forceinline__ void finish_row(const DenseArgs &a, const DenseItem &
             const int64_t pos = it.first_pos + stream * T + my_token;
             const int64_t t0 = max(it.first_pos + 1, (int64_t)it.kt0 * kDenseTile);
             const int64_t t1 = min(pos + 1, (int64_t)it.kt1 * kDenseTile);
+            const unsigned short *values = reinterpret_cast<const unsigned short *>(a.v);
             for (int64_t t = t0; t < t1; ++t) {
                 const int64_t vr = dense_row(a, it.b, it.off, t);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const float y = vr < 0 ? 0.0f : __bfloat162float(a.v[vr * a.st + it.g * a.sh + x + e]);
+                    const float y = vr < 0 ? 0.0f : bf16_lo(__ldcg(values + vr * a.st + it.g * a.sh + x + e));
                     if (!isfinite(y))
                         o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
                 }
@@ -377,8 +378,12 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
 #pragma unroll 1
             for (int again = 0; again < 2; ++again) {
                 if (__any_sync(0xffffffffu, raise)) {
-                    // (to begin with, 32 scores that the row sees are enough)
-                    const float top = tile_top(ts, negative, limit, kt == kt0 && !again ? 1 : 4);
+                    // (to begin with, 32 scores that the row sees are enough,
+                    // unless they are all -inf)
+                    const bool few = kt == kt0 && !again;
+                    float top = tile_top(ts, negative, limit, few ? 1 : 4);
+                    if (few && __any_sync(0xffffffffu, raise && limit > 32 && top == -INFINITY))
+                        top = tile_top(ts, negative, limit, 4);
                     float f = 1.0f;
                     if (raise && top > m) {
                         f = ex2((m - top) * c);

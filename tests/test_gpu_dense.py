@@ -469,3 +469,20 @@ def test_ragged_batches_at_random():
         else:
             buf = attend(k, v, off, q, q_off, h_q)
         check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
+
+
+@pytest.mark.parametrize("fresh", [1, 2, 100, 400])
+@pytest.mark.parametrize("first", [3, 40, 128, 200])
+def test_scores_of_minus_infinity(first, fresh):
+    """Keys whose scores are -inf weigh nothing, the first tokens' too: as if
+    the sequence began behind them (for rows that see others)."""
+    n, h_q, h_kv, d = 600, 14, 2, 128
+    off, q_off, q, k, v = inputs([n], [fresh], h_q, h_kv, d, 41)
+    q[:, :, 3] = q[:, :, 3].abs() + 1
+    k[:first, :, 3] = float("-inf")
+    buf = attend(k, v, off, q, q_off, h_q)
+    check([(k[first:], v[first:])], q_off, q, buf.out, buf.lse)
+    low = k.clone()
+    low[:first, :, 3] = torch.finfo(torch.bfloat16).min      # so far below the others that they weigh 0
+    again = attend(low, v, off, q, q_off, h_q)
+    check([(k[first:], v[first:])], q_off, q, again.out, again.lse)
