@@ -380,10 +380,13 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
                 if (__any_sync(0xffffffffu, raise)) {
                     // (to begin with, 32 scores that the row sees are enough,
                     // unless they are all -inf)
-                    const bool few = kt == kt0 && !again;
-                    float top = tile_top(ts, negative, limit, few ? 1 : 4);
-                    if (few && __any_sync(0xffffffffu, raise && limit > 32 && top == -INFINITY))
-                        top = tile_top(ts, negative, limit, 4);
+                    float top;
+#pragma unroll 1
+                    for (int chunks = kt == kt0 && !again ? 1 : 4;; chunks = 4) {
+                        top = tile_top(ts, negative, limit, chunks);
+                        if (chunks == 4 || !__any_sync(0xffffffffu, raise && limit > 32 && top == -INFINITY))
+                            break;
+                    }
                     float f = 1.0f;
                     if (raise && top > m) {
                         f = ex2((m - top) * c);
