@@ -325,6 +325,24 @@ __device__ __forceinline__ float tile_top(uint32_t ts, bool negative, int limit,
     return fmaxf(top[0], top[1]);
 }
 
+// O of this thread's row times f.  Stores to TMEM are asynchronous: a tile that
+// is done again may come here a second time, so they are waited for.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t to, float f)
+{
+#pragma unroll 1
+    for (int x = 0; x < D; x += 16) {
+        uint32_t o[16];
+        tmem_ld_32x32b<16>(to + x, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st16(to + x, o);
+    }
+    tmem_wait_st();
+}
+
 // ---- the softmax of one stream: 128 threads, one row each -------------------
 // A row's reference m is the largest of the first scores that it sees.  A tile's
 // weights are taken with m as it stands: they may grow above 1, and their sum
@@ -393,18 +411,8 @@ __device__ __forceinline__ void softmax_stream(const DenseArgs &a, TcShared &sh,
                         m = top;
                     }
                     l *= f;
-                    if (kt > kt0) {                  // O of this row times f
-#pragma unroll 1
-                        for (int x = 0; x < D; x += 16) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b<16>(to + x, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(to + x, o);
-                        }
-                    }
+                    if (kt > kt0)
+                        rescale_row<D>(to, f);
                 }
                 sum = kt >= masked_from ? tile_weights<true>(ts, m, c, negative, limit, p)
                                         : tile_weights<false>(ts, m, c, negative, limit, p);

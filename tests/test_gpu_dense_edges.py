@@ -1,0 +1,29 @@
+"""ts_dense_attn where a row's scores, values or cache are out of the ordinary:
+against the definition in 64 bits of test_gpu_dense.py, with its bounds."""
+import pytest
+import torch
+
+import gpu_helpers as H  # noqa: F401  (loads the library or fails)
+from test_gpu_dense import attend, definition, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fresh", [2, 60, 400])
+@pytest.mark.parametrize("first", [40, 128])
+def test_a_tile_done_again_beside_rows_without_a_reference(first, fresh):
+    """Every other head's scores of the first tokens are -inf, so that it has no
+    reference yet at the second tile, where the other heads' scores rise 45
+    above theirs: their sums so far are rescaled twice at one tile."""
+    n, h_q, h_kv, d = 600, 14, 2, 128
+    off, q_off, q, k, v = inputs([n], [fresh], h_q, h_kv, d, 43)
+    k[:first, :, 3] = -3e38
+    k[first:, :, 3] = 0
+    q[:, ::2, 3], q[:, 1::2, 3] = 0, 1e5
+    k[:128, :, 5], k[128:, :, 5] = 0, 64
+    q[:, :, 5] = 8
+    buf = attend(k, v, off, q, q_off, h_q)
+    for heads, behind in ((slice(0, None, 2), 0), (slice(1, None, 2), first)):
+        want, want_lse, tol, tol_lse = (x[:, heads] for x in definition(q, k[behind:], v[behind:], n - behind))
+        assert ((buf.out[:, heads].double() - want).abs() <= tol).all()
+        assert ((buf.lse[:, heads].double() - want_lse).abs() <= tol_lse).all()
