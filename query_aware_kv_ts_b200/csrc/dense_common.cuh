@@ -648,7 +648,8 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
 // M = max m_p:
 //   O = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p
 // in piece order, to row `at` (query row x head) of the output.  32 pieces a
-// round trip, F pieces' rows in flight.
+// round trip, F pieces' rows in flight.  A piece whose factor is 0 counts too:
+// a NaN or infinity that the row sees there has to stay.
 template <int D, int F>
 __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int head, int last, int row, int64_t at, int lane)
 {
@@ -689,7 +690,7 @@ __device__ __forceinline__ void dense_join_row(const DenseArgs &a, int head, int
                 L += __shfl_sync(0xffffffffu, l, j0 + j);
 #pragma unroll
                 for (int e = 0; e < C / 2; ++e)
-                    x[j][e] = wj[j] != 0.0f
+                    x[j][e] = j0 + j < count
                                   ? __ldcg(reinterpret_cast<const float2 *>(piece(q0 + j0 + j) + lane * C) + e)
                                   : make_float2(0.0f, 0.0f);
             }

@@ -247,14 +247,14 @@ __device__ __forceinline__ void attend_items(const DenseArgs &a, OneShared &sh, 
                 const float *src = join + (w * ROWS + row) * PS;
                 // (a maximum of -inf with a sum: every score seen was NaN)
                 const float f = mw[w] == -INFINITY ? (src[D + 1] == 0.0f ? 0.0f : 1.0f) : ex2(mw[w] - M);
-                if (f != 0.0f) {
-                    L += f * src[D + 1];
+                // (also where f is 0: times a NaN or infinity of what the row
+                // sees it is NaN, which has to stay)
+                L += f * src[D + 1];
 #pragma unroll
-                    for (int i = 0; i < D / 32; i += 2) {
-                        const float2 x = *reinterpret_cast<const float2 *>(src + lane * (D / 32) + i);
-                        acc[i] += f * x.x;
-                        acc[i + 1] += f * x.y;
-                    }
+                for (int i = 0; i < D / 32; i += 2) {
+                    const float2 x = *reinterpret_cast<const float2 *>(src + lane * (D / 32) + i);
+                    acc[i] += f * x.x;
+                    acc[i + 1] += f * x.y;
                 }
             }
             if (part_slot < 0) {

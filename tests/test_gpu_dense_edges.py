@@ -27,3 +27,33 @@ def test_a_tile_done_again_beside_rows_without_a_reference(first, fresh):
         want, want_lse, tol, tol_lse = (x[:, heads] for x in definition(q, k[behind:], v[behind:], n - behind))
         assert ((buf.out[:, heads].double() - want).abs() <= tol).all()
         assert ((buf.lse[:, heads].double() - want_lse).abs() <= tol_lse).all()
+
+
+@pytest.mark.parametrize("fresh", [1, 40])
+@pytest.mark.parametrize("n,low", [(120, (16, 32)), (700, (128, 384)), (5000, (0, 2000)), (5000, (3000, 4200))], ids=str)
+@pytest.mark.parametrize("h_q", [14, 32])
+def test_what_a_row_sees_far_below_its_maximum_stays_visible(h_q, n, low, fresh):
+    """A NaN in K, or a NaN or infinity in V, of a token whose neighbours' scores
+    lie 135 below the others': their weights are 0 in fp32, but the row does
+    see the token, wherever the work was cut."""
+    h_kv, d = 2, 128
+    off, q_off, q, k, v = inputs([n], [fresh], h_q, h_kv, d, 47)
+    q[:, :, 5] = 8
+    k[:, :, 5] = 0
+    k[low[0]:low[1], :, 5] = -192
+    clean = attend(k, v, off, q, q_off, h_q)
+    assert clean.out.isfinite().all()
+    at = (low[0] + low[1]) // 2
+    for what in ("k_nan", "v_nan", "v_inf"):
+        k2, v2 = k.clone(), v.clone()
+        if what == "k_nan":
+            k2[at] = float("nan")
+        else:
+            v2[at, :, 7] = float("nan") if what == "v_nan" else float("inf")
+        buf = attend(k2, v2, off, q, q_off, h_q)
+        if what == "k_nan":
+            assert buf.out.isnan().all() and buf.lse.isnan().all()
+        else:
+            assert not buf.out[:, :, 7].isfinite().any(), what
+            rest = [c for c in range(d) if c != 7]
+            assert torch.equal(buf.out[:, :, rest], clean.out[:, :, rest]) and torch.equal(buf.lse, clean.lse)
