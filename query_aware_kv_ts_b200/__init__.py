@@ -580,8 +580,9 @@ class DenseBuffers:
 
     def __init__(self, kv: KVCache, q_offsets):
         dev = kv.k.device
-        self.q_offsets_host = _host_offsets(q_offsets.cpu() if isinstance(q_offsets, torch.Tensor) else q_offsets,
-                                            kv.batch)
+        # (a copy: the caller's array may change, these offsets are the device's)
+        off = q_offsets.cpu() if isinstance(q_offsets, torch.Tensor) else q_offsets
+        self.q_offsets_host = _host_offsets(off, kv.batch).copy()
         self.q_offsets_dev = torch.from_numpy(self.q_offsets_host).to(dev)
         self.rows = int(self.q_offsets_host[-1])
         self.ws = torch.empty(ts_dense_attn_workspace_bytes(kv, self.q_offsets_host), dtype=torch.uint8, device=dev)

@@ -1,0 +1,30 @@
+"""What the binding of the new-token calls keeps and refuses, without a GPU: the
+library's own calls are replaced where they would need one."""
+import numpy as np
+import pytest
+import torch
+
+
+@pytest.fixture
+def ts(monkeypatch):
+    import query_aware_kv_ts_b200 as m
+    monkeypatch.setattr(m, "ts_dense_attn_workspace_bytes", lambda kv, off: 1024)
+    monkeypatch.setattr(m, "ts_workspace_init", lambda ws, stream=None: None)
+    return m
+
+
+def cache(ts, n=40, batch=2):
+    rows = torch.zeros((n, 2, 64), dtype=torch.bfloat16)
+    return ts.KVCache(rows, rows.clone(), np.linspace(0, n, batch + 1).astype(np.int64), 8)
+
+
+@pytest.mark.parametrize("kind", ["array", "tensor", "list"])
+def test_buffers_keep_the_offsets_they_were_made_for(ts, kind):
+    """A serving loop may update its own offsets in place: the buffers' host and
+    device copies stay equal to each other."""
+    own = {"array": np.array, "tensor": torch.tensor, "list": list}[kind]([0, 3, 7])
+    buf = ts.DenseBuffers(cache(ts), own)
+    for b in (1, 2):
+        own[b] = b
+    assert buf.q_offsets_host.tolist() == [0, 3, 7] == buf.q_offsets_dev.tolist()
+    assert buf.rows == 7 and buf.out.shape[0] == 7
