@@ -400,8 +400,10 @@ TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, 
  *                  but ts_get_device_status, which reads it; one of the
  *                  largest size serves calls of several shapes in turn
  * The cache may be packed, growing (capacity; the length is read on the
- * device) or paged (a table entry outside the pool: no access outside the
- * pool, results not defined).  At most 2^24 query rows.
+ * device) or paged (a table entry outside the pool, or a length on the device
+ * that passes the table's row or the cache: no access outside the table, the
+ * pool and the cache, results of that sequence not defined).  At most 2^24
+ * query rows.
  */
 TS_API size_t ts_dense_attn_workspace_bytes(const ts_kv_t *kv, const int64_t *q_offsets_host);
 TS_API ts_status_t ts_dense_attn(const ts_kv_t *kv, const void *q, int64_t q_stride_tok, const int64_t *q_offsets,

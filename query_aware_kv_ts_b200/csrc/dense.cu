@@ -125,6 +125,7 @@ ts_status_t launch_dense(const DensePlan &dp, const ts_kv_t *kv, const void *q, 
     a.pt_stride = kv->page_table_stride;
     a.page_shift = p.page_shift;
     a.pool_pages = kv->pool_pages;
+    a.kv_rows = p.kv_rows;
 
     // K and V boxes: 64 channels x 128 tokens of one kv head; of a paged cache
     // the rows of a page (128 tokens of it at most), with head_dim 128 as

@@ -56,6 +56,7 @@ struct DenseArgs {
     const int32_t *page_table;
     int pt_stride, page_shift;
     int64_t pool_pages;
+    int64_t kv_rows;      // token rows of the cache (of the pool)
     // K and V tiles in shared memory: rows of 64 channels (128 bytes, 128-byte
     // swizzle), 8 tokens together; bytes from 8 tokens to the next 8, and from
     // the first 64 channels to the others.  A paged cache's boxes hold whole
@@ -368,15 +369,23 @@ __device__ __forceinline__ void dense_begin(const DenseArgs &a, void *smem, int 
     __syncwarp();
 }
 
-// The K / V row of token i < n of a sequence; -1 on a page outside the pool.
+// The pool's page with token i of sequence b; -1 for an entry outside the pool,
+// and behind the table's row (device lengths may pass what the host's said).
+__device__ __forceinline__ int32_t dense_page(const DenseArgs &a, int b, int64_t i)
+{
+    const int64_t j = i >> a.page_shift;
+    const int32_t pg = j < a.pt_stride ? __ldcg(a.page_table + (int64_t)b * a.pt_stride + j) : -1;
+    return pg < a.pool_pages ? pg : -1;
+}
+
+// The K / V row of token i of a sequence that begins at row off (packed); -1
+// where the cache has none.
 __device__ __forceinline__ int64_t dense_row(const DenseArgs &a, int b, int64_t off, int64_t i)
 {
     if (a.page_table == nullptr)
-        return off + i;
-    const int32_t pg = __ldcg(a.page_table + (int64_t)b * a.pt_stride + (i >> a.page_shift));
-    if (pg < 0 || pg >= a.pool_pages)
-        return -1;
-    return ((int64_t)pg << a.page_shift) + (i & (((int64_t)1 << a.page_shift) - 1));
+        return off + i < a.kv_rows ? off + i : -1;
+    const int32_t pg = dense_page(a, b, i);
+    return pg < 0 ? -1 : ((int64_t)pg << a.page_shift) + (i & (((int64_t)1 << a.page_shift) - 1));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -572,8 +581,8 @@ __device__ __forceinline__ void load_items(const DenseArgs &a, DenseRing<MAXNS> 
                 const int64_t i = ((int64_t)kt << 7) + ((int64_t)lane << a.box_shift);
                 row = oob;
                 if (i < it.n) {
-                    const int32_t pg = __ldcg(a.page_table + (int64_t)it.b * a.pt_stride + (i >> a.page_shift));
-                    if (pg >= 0 && pg < a.pool_pages)
+                    const int32_t pg = dense_page(a, it.b, i);
+                    if (pg >= 0)
                         row = (pg << a.page_shift) + (int32_t)(i & ((1 << a.page_shift) - 1));
                 }
             }

@@ -3,8 +3,8 @@ against the definition in 64 bits of test_gpu_dense.py, with its bounds."""
 import pytest
 import torch
 
-import gpu_helpers as H  # noqa: F401  (loads the library or fails)
-from test_gpu_dense import attend, definition, inputs
+import gpu_helpers as H
+from test_gpu_dense import attend, check, definition, inputs, paged, sequences
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,29 @@ def test_what_a_row_sees_far_below_its_maximum_stays_visible(h_q, n, low, fresh)
             assert not buf.out[:, :, 7].isfinite().any(), what
             rest = [c for c in range(d) if c != 7]
             assert torch.equal(buf.out[:, :, rest], clean.out[:, :, rest]) and torch.equal(buf.lse, clean.lse)
+
+
+@pytest.mark.parametrize("fresh", [1, 30])
+@pytest.mark.parametrize("page", [16, 256])
+def test_lengths_on_the_device_that_pass_the_block_table(page, fresh):
+    """What stands in memory behind a sequence's row of the table is not taken
+    for its pages: here they would be pages of NaN."""
+    m = H.ts()
+    h_q, h_kv, d, n, stride = 8, 2, 128, 4 * page, 4
+    off, q_off, q, k, v = inputs([n], [fresh], h_q, h_kv, d, 51)
+    kp, vp, table = paged(k, v, off, page, 1)
+    owned = set(table.flatten().tolist())
+    stray = next(p for p in range(kp.shape[0] // page) if p not in owned)
+    around = torch.full((64 * stride,), stray, dtype=torch.int32, device="cuda")
+    around[:stride] = table.flatten()
+    kv = m.KVCache(kp, vp, off, h_q, page_table=around[:stride].view(1, stride), page_size=page)
+    buf = m.DenseBuffers(kv, q_off)
+    kv.seq_offsets_dev[1] = n + 20 * page
+    m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
+    torch.cuda.synchronize()
+    assert m.ts_get_device_status(buf.ws) == (m.TS_OK, 0)
+    assert buf.out.isfinite().all() and buf.lse.isfinite().all()
+    kv.seq_offsets_dev[1] = n
+    m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
+    torch.cuda.synchronize()
+    check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
