@@ -399,6 +399,11 @@ TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, 
  *                  once (ts_workspace_init) and used by no other entry point
  *                  but ts_get_device_status, which reads it; one of the
  *                  largest size serves calls of several shapes in turn
+ * Lengths, offsets and block table are read on the device.  A captured call
+ * on a growing or paged cache serves other lengths and pages, as long as the
+ * query offsets stay; the host's lengths at capture size its launch only
+ * (those of a paged cache may be the longest to come: short ones leave long
+ * sequences to few blocks, with the same results up to the split of the work).
  * The cache may be packed, growing (capacity; the length is read on the
  * device) or paged (a table entry outside the pool, or a length on the device
  * that passes the table's row or the cache: no access outside the table, the

@@ -1,9 +1,11 @@
 """ts_dense_attn where a row's scores, values or cache are out of the ordinary:
 against the definition in 64 bits of test_gpu_dense.py, with its bounds."""
+import numpy as np
 import pytest
 import torch
 
 import gpu_helpers as H
+import workloads as W
 from test_gpu_dense import attend, check, definition, inputs, paged, sequences
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +85,73 @@ def test_lengths_on_the_device_that_pass_the_block_table(page, fresh):
     m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
     torch.cuda.synchronize()
     check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
+
+
+@pytest.mark.parametrize("longest", [True, False])
+@pytest.mark.parametrize("fresh", [[1, 1, 1], [1, 0, 5], [2, 40, 1]], ids=str)
+def test_a_captured_step_of_a_growing_paged_batch(fresh, longest):
+    """One graph of [room, rows, attention] on a paged batch: the lengths grow on
+    the device from replay to replay.  Captured with the longest lengths to
+    come in the host's offsets, or with the first ones."""
+    m = H.ts()
+    h_q, h_kv, d, page, steps = 28, 4, 128, 16, 30
+    start = np.array([700, 5, 130])
+    fresh = np.array(fresh)
+    end = start + (steps + 1) * fresh
+    stride = int(-(-end.max() // page))
+    pool = int((-(-end // page)).sum()) + 7
+    g = torch.Generator(device="cuda").manual_seed(61)
+    new = [torch.randn((steps + 1, int(fresh.sum()), h, d), device="cuda", generator=g).to(torch.bfloat16) for h in (h_q, h_kv, h_kv)]
+    first = [[torch.randn((int(n), h_kv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2)] for n in start]
+    pool_k = torch.full((pool * page, h_kv, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    pool_v = pool_k.clone()
+    dev = {"dtype": torch.int64, "device": "cuda"}
+    order = torch.randperm(pool, generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda()
+    table = torch.full((3, stride), -1, dtype=torch.int32, device="cuda")
+    host = W.seq_offsets(end if longest else start)
+    kv = m.KVCache(pool_k, pool_v, host, h_q, page_table=table, page_size=page)
+    buf = m.DenseBuffers(kv, W.seq_offsets(fresh))
+    cached, count, used = torch.zeros(3, **dev), torch.from_numpy(start).cuda(), torch.zeros(1, **dev)
+    slots = torch.zeros(int(start.sum()), **dev)
+    qo = torch.zeros(4, **dev)
+    m.ts_extend_pages(cached, count, page, order, pool, table, kv.seq_offsets_dev, qo, slots, used)
+    m.ts_write_kv(kv, torch.cat([x[0] for x in first]), torch.cat([x[1] for x in first]), slots)
+    torch.cuda.synchronize()
+    taken = int(used)
+    cached.copy_(count)
+    count.copy_(torch.from_numpy(fresh))
+    free, slots = order.clone(), torch.zeros(int(fresh.sum()), **dev)
+    q, kn, vn = (x[0].clone() for x in new)
+
+    def step():
+        m.ts_extend_pages(cached, count, page, free, pool, table, kv.seq_offsets_dev, buf.q_offsets_dev, slots, used)
+        m.chunk_step(kv, q, kn, vn, slots, buf)
+        cached.add_(count)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    for i in range(steps + 1):
+        free[:pool - taken] = order[taken:]
+        for to, x in zip((q, kn, vn), new):
+            to.copy_(x[i])
+        torch.cuda.synchronize()
+        if i == 0:
+            with torch.cuda.stream(s):
+                step()                     # warm-up
+                s.synchronize()
+                with torch.cuda.graph(graph, stream=s):
+                    step()
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        taken += int(used)
+        lengths = start + (i + 1) * fresh
+        assert cached.tolist() == lengths.tolist() and kv.seq_offsets_dev.tolist() == W.seq_offsets(lengths).tolist()
+        if i % 7 and i != steps:
+            continue
+        at = W.seq_offsets(fresh)
+        rows = [tuple(torch.cat([first[b][c]] + [x[j, int(at[b]):int(at[b + 1])] for j in range(i + 1)]) for c, x in ((0, new[1]), (1, new[2])))
+                for b in range(3)]
+        check(rows, at, q, buf.out, buf.lse)
+    assert m.ts_get_device_status(buf.ws) == (m.TS_OK, 0)
