@@ -146,6 +146,8 @@ class KVCache:
             raise TypeError("K and V must be bf16")
         if k.dim() != 3 or k.shape != v.shape or k.stride() != v.stride() or k.stride(2) != 1:
             raise ValueError("K and V must be [tokens, h_kv, d] with equal strides and contiguous channels")
+        if v.device != k.device or (page_table is not None and page_table.device != k.device):
+            raise ValueError("K, V and page_table must be on one device")
         off = np.ascontiguousarray(np.asarray(seq_offsets.cpu() if isinstance(seq_offsets, torch.Tensor)
                                               else seq_offsets, dtype=np.int64))
         self.k, self.v = k, v
@@ -157,6 +159,8 @@ class KVCache:
         if page_table is not None:
             if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
                 raise ValueError("page_table must be a contiguous int32 [batch, stride] tensor")
+            if page_table.shape[0] < self.batch:
+                raise ValueError("page_table has %d rows for %d sequences" % (page_table.shape[0], self.batch))
             if page_size <= 0 or k.shape[0] % page_size:
                 raise ValueError("page_size must divide the pool's rows")
             stride, pool_pages, table_ptr = page_table.shape[1], k.shape[0] // page_size, page_table.data_ptr()

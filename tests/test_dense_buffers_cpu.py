@@ -28,3 +28,18 @@ def test_buffers_keep_the_offsets_they_were_made_for(ts, kind):
         own[b] = b
     assert buf.q_offsets_host.tolist() == [0, 3, 7] == buf.q_offsets_dev.tolist()
     assert buf.rows == 7 and buf.out.shape[0] == 7
+
+
+def test_a_cache_refuses_parts_on_another_device_and_short_tables(ts):
+    """K decides where the calls run: V and the block table have to be there, and
+    the table needs a row for every sequence."""
+    k = torch.zeros((32, 2, 64), dtype=torch.bfloat16)
+    table = torch.zeros((2, 2), dtype=torch.int32)
+    kept = ts.KVCache(k, k.clone(), [0, 16, 32], 8, page_table=table, page_size=16)
+    assert kept.struct.page_table_stride == 2
+    with pytest.raises(ValueError, match="device"):
+        ts.KVCache(k, k.to("meta"), [0, 32], 8)
+    with pytest.raises(ValueError, match="device"):
+        ts.KVCache(k, k.clone(), [0, 16, 32], 8, page_table=table.to("meta"), page_size=16)
+    with pytest.raises(ValueError, match="sequences"):
+        ts.KVCache(k, k.clone(), [0, 8, 16, 32], 8, page_table=table, page_size=16)
