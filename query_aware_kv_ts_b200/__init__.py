@@ -150,6 +150,9 @@ class KVCache:
             raise ValueError("K, V and page_table must be on one device")
         off = np.ascontiguousarray(np.asarray(seq_offsets.cpu() if isinstance(seq_offsets, torch.Tensor)
                                               else seq_offsets, dtype=np.int64))
+        if page_table is None and max(int(off[-1]), int(capacity)) > k.shape[0]:
+            raise ValueError("K and V hold %d rows, the offsets and capacity need %d" %
+                             (k.shape[0], max(int(off[-1]), int(capacity))))
         self.k, self.v = k, v
         self.seq_offsets_host = off
         self.seq_offsets_dev = torch.from_numpy(off).to(k.device)

@@ -43,3 +43,14 @@ def test_a_cache_refuses_parts_on_another_device_and_short_tables(ts):
         ts.KVCache(k, k.clone(), [0, 16, 32], 8, page_table=table.to("meta"), page_size=16)
     with pytest.raises(ValueError, match="sequences"):
         ts.KVCache(k, k.clone(), [0, 8, 16, 32], 8, page_table=table, page_size=16)
+
+
+def test_a_cache_refuses_offsets_that_pass_its_rows(ts):
+    k = torch.zeros((32, 2, 64), dtype=torch.bfloat16)
+    for off, capacity in (([0, 32], 0), ([0, 10], 32), ([0, 0], 0)):
+        ts.KVCache(k, k.clone(), off, 8, capacity=capacity)
+    for off, capacity in (([0, 33], 0), ([0, 10], 33)):
+        with pytest.raises(ValueError, match="rows"):
+            ts.KVCache(k, k.clone(), off, 8, capacity=capacity)
+    table = torch.zeros((1, 4), dtype=torch.int32)
+    ts.KVCache(k, k.clone(), [0, 60], 8, page_table=table, page_size=16)       # pages may be shared
