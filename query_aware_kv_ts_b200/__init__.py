@@ -492,10 +492,11 @@ def ts_dense_attn(kv: KVCache, q, q_offsets_dev, q_offsets_host, out, lse, ws, s
         raise ValueError("q, out and lse must hold the %d query rows" % rows)
     if not (q_offsets_dev.dtype is _I64 and out.dtype is _BF16 and q_offsets_dev.get_device() == dev and
             out.get_device() == dev and ws.get_device() == dev and q_offsets_dev.is_contiguous() and
-            out.is_contiguous() and q_offsets_dev.numel() == B + 1 and out.shape == (n_out, h_q, d)):
+            out.is_contiguous() and q_offsets_dev.numel() == B + 1 and out.shape == (n_out, h_q, d) and
+            ws.is_contiguous()):
         _refuse("q_offsets_dev", q_offsets_dev, _I64, dev, (B + 1,))
         _refuse("out", out, _BF16, dev, (n_out, h_q, d))
-        _wrong_device("ws", ws, dev)
+        _refuse("ws", ws, ws.dtype, dev, ws.shape)
     if lse is not None:
         if not (lse.dtype is torch.float32 and lse.get_device() == dev and lse.is_contiguous() and
                 lse.shape == (lse.shape[0], h_q)):

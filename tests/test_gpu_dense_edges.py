@@ -155,3 +155,20 @@ def test_a_captured_step_of_a_growing_paged_batch(fresh, longest):
                 for b in range(3)]
         check(rows, at, q, buf.out, buf.lse)
     assert m.ts_get_device_status(buf.ws) == (m.TS_OK, 0)
+
+
+def test_a_workspace_with_fewer_bytes_than_elements_is_refused():
+    """An expanded or strided tensor counts elements that it does not hold."""
+    m = H.ts()
+    off, q_off, q, k, v = inputs([40], [40], 8, 2, 64, 5)
+    kv = m.KVCache(k, v, off, 8)
+    buf = m.DenseBuffers(kv, q_off)
+    n = buf.ws.numel()
+    for ws in (buf.ws[:1].expand(n), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, ws)
+    with pytest.raises(m.TsError, match="too small"):
+        m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws[:n - 256])
+    m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
+    torch.cuda.synchronize()
+    check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
