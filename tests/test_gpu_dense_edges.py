@@ -172,3 +172,55 @@ def test_a_workspace_with_fewer_bytes_than_elements_is_refused():
     m.ts_dense_attn(kv, q, buf.q_offsets_dev, buf.q_offsets_host, buf.out, buf.lse, buf.ws)
     torch.cuda.synchronize()
     check(sequences(k, v, off), q_off, q, buf.out, buf.lse)
+
+
+def cancelling(lengths, h_q, h_kv, d, seed):
+    """One query token a sequence whose weights nearly cancel in V, so that the
+    output's own rounding hides nothing: 16 tokens with weights of one size and
+    a heavier one whose V takes their sum away (channel c: for head c % G of its
+    kv head), the others 40 and more below them.  K has one channel, so the
+    scores are one exact product each.  On the CPU, from the seed alone."""
+    g = torch.Generator().manual_seed(seed)
+    G, scale = h_q // h_kv, d ** -0.5
+    B, off = len(lengths), W.seq_offsets(lengths)
+    q = torch.zeros((B, h_q, d), dtype=torch.bfloat16)
+    q[:, :, 0] = 1 + torch.rand((B, h_q), generator=g)
+    k = torch.zeros((int(off[-1]), h_kv, d), dtype=torch.bfloat16)
+    v = torch.randn(k.shape, generator=g).to(torch.bfloat16)
+    k[:, :, 0] = -1000
+    want = torch.zeros((B, h_q, d), dtype=torch.float64)
+    size, plain_bf16 = torch.zeros_like(want), torch.zeros_like(want)      # sum w |V|; with weights of 8 bits
+    for b in range(B):
+        at = int(off[b]) + torch.randperm(int(lengths[b]), generator=g)[:17]
+        for h in range(h_kv):
+            k[at, h, 0] = torch.cat([torch.rand(16, generator=g) * 12 - 8, torch.tensor([8.0])]).to(torch.bfloat16)
+            s = q[b, h * G:(h + 1) * G, 0].double().unsqueeze(1) * k[at, h, 0].double() * scale
+            e = torch.exp(s - s.amax(1, keepdim=True))
+            w = e / e.sum(1, keepdim=True)
+            for c in range(d):
+                v[at[16], h, c] = -(w[c % G, :16] @ v[at[:16], h, c].double()) / w[c % G, 16]
+            rows, vv = slice(h * G, (h + 1) * G), v[at, h].double()
+            want[b, rows], size[b, rows] = w @ vv, w @ vv.abs()
+            plain_bf16[b, rows] = e.to(torch.bfloat16).double() @ vv / e.sum(1, keepdim=True)
+    return off, q, k, v, want, size, plain_bf16
+
+
+@pytest.mark.parametrize("lengths", [[60], [1000], [300, 17, 128, 129] * 10], ids=["whole", "shared", "many"])
+@pytest.mark.parametrize("heads", [(28, 4, 128), (8, 1, 128), (32, 2, 128), (12, 1, 128), (4, 2, 64), (16, 1, 64)], ids=str)
+def test_the_weights_of_one_token_are_a_bf16_and_its_remainder(heads, lengths):
+    """Up to 8 heads a group a weight's bf16 is off by 2^-8 of it and the
+    remainder's by 2^-8 of that: 2^-16.  Above, the first is cut off (2^-7):
+    2^-15.  The rest as in test_gpu_dense.py, the scores being one exact product
+    and its scaling (at most 2 in size): n 2^-23 for the sums, 2^-20 for the
+    exponentials and the normaliser, 2 x 2 x 2^-22 for the scaling.  Weights
+    40 below add less than 2^-40.  Weights without their remainder (the oracle's)
+    are far outside."""
+    h_q, h_kv, d = heads
+    off, q, k, v, want, size, plain_bf16 = cancelling(lengths, h_q, h_kv, d, 71)
+    n = torch.tensor(lengths, dtype=torch.float64).view(-1, 1, 1)
+    weight = 2.0 ** -16 if h_q // h_kv <= 8 else 2.0 ** -15
+    tol = size * (weight + n * 2.0 ** -23 + 2.0 ** -19) + want.abs() * 2.0 ** -8
+    assert ((plain_bf16 - want).abs() > tol).double().mean() > 0.25
+    buf = attend(k.cuda(), v.cuda(), off, q.cuda(), list(range(len(lengths) + 1)), h_q)
+    err = (buf.out.double().cpu() - want).abs()
+    assert (err <= tol).all(), "worst %.3g of the bound" % float((err / tol).max())
