@@ -381,7 +381,8 @@ TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, 
  *   lse[r,h]   = log sum_{j <= p} exp(scale * q[r,h,:] . K[b,j,h/G,:])
  * with r = q_offsets[b] + i.  f_b = n_b is a whole prompt, f_b = 1 a decode
  * step, f_b = 0 a sequence without queries; they may stand side by side.  A
- * row that sees nothing (p < 0) gives zeros and -inf.  The scores, their
+ * row that sees nothing (p < 0), or whose scores are all -inf, gives zeros and
+ * -inf; one that sees a score of NaN or +inf, NaN in out and lse.  The scores, their
  * reference and sum and the weighted sums are fp32; the weights are rounded to
  * bf16 for the product with V (with f_b = 1 as a bf16 and its bf16 remainder),
  * and out at the end.  Tokens that a row does not see have no effect on it,
@@ -405,10 +406,10 @@ TS_API ts_status_t ts_write_kv(const ts_kv_t *kv, void *k_cache, void *v_cache, 
  * (those of a paged cache may be the longest to come: short ones leave long
  * sequences to few blocks, with the same results up to the split of the work).
  * The cache may be packed, growing (capacity; the length is read on the
- * device) or paged (a table entry outside the pool, or a length on the device
- * that passes the table's row or the cache: no access outside the table, the
- * pool and the cache, results of that sequence not defined).  At most 2^24
- * query rows.
+ * device) or paged.  A table entry outside the pool, or a length on the device
+ * that passes the table's row or the cache (up to the 4,194,304 tokens that a
+ * sequence may have): no access outside the table, the pool and the cache,
+ * results of that sequence not defined.  At most 2^24 query rows.
  */
 TS_API size_t ts_dense_attn_workspace_bytes(const ts_kv_t *kv, const int64_t *q_offsets_host);
 TS_API ts_status_t ts_dense_attn(const ts_kv_t *kv, const void *q, int64_t q_stride_tok, const int64_t *q_offsets,

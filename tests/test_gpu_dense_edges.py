@@ -224,3 +224,29 @@ def test_the_weights_of_one_token_are_a_bf16_and_its_remainder(heads, lengths):
     buf = attend(k.cuda(), v.cuda(), off, q.cuda(), list(range(len(lengths) + 1)), h_q)
     err = (buf.out.double().cpu() - want).abs()
     assert (err <= tol).all(), "worst %.3g of the bound" % float((err / tol).max())
+
+
+@pytest.mark.parametrize("fresh", [1, 2, 200])
+@pytest.mark.parametrize("n", [100, 200, 3100])
+@pytest.mark.parametrize("h_q", [14, 32])
+def test_rows_of_infinite_scores(h_q, n, fresh):
+    """Scores that are all -inf leave nothing: zeros and -inf.  One of +inf, like
+    one of NaN, makes the row NaN."""
+    h_kv, d = 2, 128
+    fresh = min(fresh, n)
+    off, q_off, q, k, v = inputs([n, 40], [fresh, 40], h_q, h_kv, d, 83)
+    clean = attend(k, v, off, q, q_off, h_q)
+    q[:fresh, :, 3] = 1
+    k2 = k.clone()
+    k2[:n, :, 3] = float("-inf")
+    buf = attend(k2, v, off, q, q_off, h_q)
+    assert (buf.out[:fresh] == 0).all() and (buf.lse[:fresh] == float("-inf")).all()
+    assert torch.equal(buf.out[fresh:], clean.out[fresh:]) and torch.equal(buf.lse[fresh:], clean.lse[fresh:])
+    at = n - fresh // 2 - 1
+    k2 = k.clone()
+    k2[at, :, 3] = float("inf")
+    buf = attend(k2, v, off, q, q_off, h_q)
+    first = at - (n - fresh)              # the first query row that sees the token
+    assert buf.out[:first].isfinite().all() and buf.lse[:first].isfinite().all()
+    assert buf.out[first:fresh].isnan().all() and buf.lse[first:fresh].isnan().all()
+    assert torch.equal(buf.out[fresh:], clean.out[fresh:]) and torch.equal(buf.lse[fresh:], clean.lse[fresh:])
