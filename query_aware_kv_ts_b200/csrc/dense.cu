@@ -14,7 +14,12 @@ namespace {
 constexpr int kMergeWarps = 8;
 
 // What an item costs beside its tokens, in tokens (half a tile for the last
-// one's rest included).
+// one's rest included).  Chosen at head_dim 128: with 200 / 400 / 650 for
+// prompts, 8192 tokens of 28/4 heads take 466 / 427 / 435 us and a mixed step
+// 517 / 458 / 460 (calls back to back); at head_dim 64 an item's end weighs
+// less (8192 tokens of 32/8: 482 / 503 / 510 us).  For single tokens
+// 96 / 192 / 400 are within 5 % of one another, except 4 requests of 1000 at
+// head_dim 64, 13.7 / 10.4 / 11.3 us.
 constexpr int kOneItemCost = 192, kTcItemCost = 400;
 
 // The shared items of dense_tc: a block of this kernel for each block of that
@@ -84,9 +89,13 @@ void plan_dense(const ts_kv_t *kv, const int64_t *q_off, DensePlan *dp)
         items *= p.Hkv;
         tiles *= p.Hkv;
         // One query token: what a block reads, it reads at some 27 bytes a
-        // clock, so a tile to a block where there are few.  Several: up to 4
-        // tiles an item is not worth cutting, its pieces' start and their join
-        // cost more than they save, and pieces have 3 tiles or more.
+        // clock, so a tile to a block where there are few.  Several: where no
+        // item has more than 4 tiles none is cut, its pieces' start and their
+        // join cost more than they save (prompts of 200 and 500 tokens, 28/4
+        // heads: 13.1 and 17.1 us whole, 20.6 and 31.6 cut; 700 and 1000
+        // tokens, 6 and 8 tiles, which are cut: 32.8 and 37.7 us, against 21.1
+        // and 27.0 whole, so the border could lie higher).  Pieces have 3
+        // tiles or more.
         w.split = one ? most > 1 : most > 4;
         const int64_t parts = !w.split ? items : (one ? tiles : (tiles + 2) / 3);
         w.grid = (int)(parts < p.sms ? (parts > 1 ? parts : items > 0) : p.sms);

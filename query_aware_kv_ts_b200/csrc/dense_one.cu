@@ -5,11 +5,14 @@
 // filled by TMA (K and V in turn), and eight warps that take 16 tokens of
 // every tile each.  Measured: one token over 1,048,576 of 4 x 128, 2.1 GB,
 // 324-335 us (98-101 % of the copy rate); 32 requests of 8192 to 65536 tokens
-// of 8 x 128 on 16-token pages, 3.0 GB, 488 us (92 %; 8-token pages, whose
-// boxes of 2 KB cost their issue, half as long again).  A block alone reads
-// about 27 bytes a clock, so a small batch goes to as many as it has tiles
-// (4 requests of about 1000 tokens: 12.6 us, 3 us of them the kernel's start
-// to its first load).  A warp keeps its own running maximum, sum and weighted
+// of 8 x 128 on 16-token pages, 3.0 GB, 489-502 us on several cards (90-92 %).
+// With calls back to back on few inputs, part of them in L2: 445 us, and 431
+// packed, 433 with 32-token pages, 625 with 8-token ones, whose boxes of 2 KB
+// cost their issue; the same batch with head_dim 64: 346 packed, 337, 397 and
+// 584 with 32-, 16- and 8-token pages (boxes of 4, 2 and 1 KB).  A block alone
+// reads about 27 bytes a clock (clock64 in a copy with counters), so a small
+// batch goes to as many as it has tiles (4 requests of about 1000 tokens:
+// 12.5 us, 3 us of them the kernel's start to its first load).  A warp keeps its own running maximum, sum and weighted
 // sums, and the eight are joined at the end of the item, so nothing in the
 // loop waits for another warp.
 //

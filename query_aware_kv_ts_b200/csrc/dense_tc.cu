@@ -15,12 +15,15 @@
 // must not leak out of V.  While one stream's softmax runs, the tensor cores
 // do the other's products.
 //
-// Measured, head_dim 128: a prompt of 8192 tokens, 28/4 heads, 491 us (980
+// Measured, head_dim 128: a prompt of 8192 tokens, 28/4 heads, 488-493 us (976
 // TFLOP/s of the causal half); 2048 new tokens over 129,025 on 16-token pages,
-// 4.0 ms (940).  A tile takes both streams 3300 cycles, of which the products
-// are 2048 and each stream's softmax 1750 (1024 exponentials' worth: the two
-// overlap in part and share the exponential unit); runs longer than some
-// 100 us are at the board's power limit (1.4-1.5 GHz of 1.965).  Tried and
+// 3.95-4.06 ms (926-951).  A tile takes both streams 3300 cycles (clock64 in a
+// copy with counters), of which the products are 2048.  What bounds it is the
+// chain inside a stream: the next S is issued behind P V and both behind P, so
+// a tile costs a stream its softmax (1750 cycles, two streams sharing the
+// exponential unit's 2048), the two products (512 each) and the hand-over;
+// runs longer than some 100 us are at the board's power limit (1.4-1.5 GHz of
+// 1.965).  Tried and
 // slower: half rows on four softmax groups with a barrier for their common
 // reference (857 against 906 TFLOP/s then), P handed over in halves to a
 // polling issuer (770 against 920), every other tile of a narrow item on the
@@ -138,7 +141,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// 32 weights 2^(s c - mc): their sum added to sum, as bf16 in p.  (A share of
+// 32 weights 2^(s c - mc): their sum added to sum, as bf16 in p.  The tensor
+// cores take P in V's type; a second product with the remainders would be 512
+// cycles more a stream and tile.  Rounding is off by 2^-8 of a weight at most,
+// in either direction, as the output's own rounding is: the error against 64
+// bits is 2.0-2.3e-3 of the norm where that alone leaves 1.6e-3.  The sum takes
+// the weights before rounding, so it has no part in it.  (A share of
 // them by a polynomial on the FMA units, beside the exponential unit, was
 // 2-5 % slower in long runs: those run at the power limit, where what counts
 // is the number of operations.)
